@@ -104,6 +104,10 @@ typedef struct {
  *   n_modules   adapted linear layers per slot, >= 1
  *   h_in,h_out  [host] [n_modules] input/output widths; multiples of page_elems
  *   max_rank    rank cap, 1..LORA_MAX_RANK
+ * An entry spans at most max_rank * (h_in + h_out) / page_elems pages, which
+ * may be up to 8192.  Pools with a module above 1024 (small pages under wide
+ * modules and high ranks) serve the fused passes only: lora_shrink,
+ * lora_expand and the lora_apply calls return LORA_ERR_SHAPE for them.
  * On success *out holds the pool.  Synchronous.  Errors: ARG, SHAPE, RANK, HIP. */
 lora_status lora_pool_create(lora_pool **out, int32_t device, lora_dtype wdtype,
                              int64_t page_elems, int64_t n_pages, int32_t n_slots,

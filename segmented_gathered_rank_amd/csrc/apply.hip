@@ -54,6 +54,7 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 // Modules module0 .. module0 + n_modules - 1 exist and share h_in (and h_out when same_out).
 lora_status check_modules(const lora_pool* p, int32_t module0, int32_t n_modules, bool same_out) {
   if (!p || n_modules < 1 || module0 < 0 || module0 + n_modules > p->n_modules) return LORA_ERR_ARG;
+  if (p->max_pages_per_entry > kMaxEntryPages) return LORA_ERR_SHAPE;   // the kernels' page-id tables in LDS
   for (int32_t m = module0 + 1; m < module0 + n_modules; ++m) {
     if (p->h_in[m] != p->h_in[module0] || (same_out && p->h_out[m] != p->h_out[module0])) return LORA_ERR_SHAPE;
   }

@@ -18,7 +18,8 @@ constexpr int kTileTokens = 64;    // tokens per matrix-core tile
 constexpr int kLongMin = 64;       // segments this long or longer use matrix-core tiles
 constexpr int kMaxRank = LORA_MAX_RANK;
 constexpr int kMaxSlots = 8192;   // the segment builder's LDS histogram bound
-constexpr int kMaxEntryPages = 1024;  // pages of one (slot, module) entry (an LDS table in the GEMV kernels)
+constexpr int kMaxEntryPages = 1024;  // pages of one (slot, module) entry the apply kernels serve (an LDS table in the GEMV ones)
+constexpr int kMaxPoolEntryPages = 8192;  // pages of one entry a pool accepts (the fused passes read any)
 
 // One (slot, module) entry of the device slot table.
 struct SlotEntry {
