@@ -422,6 +422,100 @@ lora_status lora_fused_gemm_fp8w(const lora_pool *p, int32_t module,
                                  const float *w_scale, const int32_t *ids, int32_t n_tokens,
                                  void *y, int64_t ld_y, void *stream);
 
+/* Workspace bytes (device, 16-byte aligned, no initialization needed) of one
+ * call of the four entry points below: n_proj is 1 for lora_fused_gemm_w4 and
+ * 2 for the gated ones, `module` one of the call's modules.  0 where the call
+ * needs none (long batches, bad arguments); a call without ids needs none
+ * either.  Calls that share a workspace must be ordered on one stream; two
+ * captured graphs that may run at the same time need one each. */
+size_t lora_fused_workspace_bytes(const lora_pool *p, int32_t module, int32_t n_proj, int32_t n_tokens);
+
+/* Base weights of one projection as 4-bit codes with a scale per output column
+ * and group of `group` consecutive k (study page, section "Operating it": a
+ * quantized base serves under the bf16 adapters; its table of adapter kinds
+ * has those trained against a 4-bit codebook base):
+ *   W[k][c] = scale[k / group][c] * v,  with the code q = q[c][k]:
+ *     v = q - 8                    zero and table NULL
+ *     v = q - zero[k / group][c]   zero given
+ *     v = table[q]                 table given (zero is then NULL)
+ * All arrays are on the device and stay the caller's. */
+typedef struct {
+    const void *codes;    /* [h_out][ld_codes] bytes: byte b of row c holds the codes of k = 2b (low
+                             four bits) and k = 2b + 1 of output column c; 16-byte aligned       */
+    int64_t ld_codes;     /* bytes from row to row: a multiple of 16, >= h_in / 2                */
+    const void *scale;    /* [h_in / group][ld_scale] bf16, 8-byte aligned                       */
+    const uint8_t *zero;  /* [h_in / group][ld_scale] bytes 0..255, 4-byte aligned, or NULL      */
+    int64_t ld_scale;     /* elements from group to group: a multiple of 4, >= h_out             */
+    const void *table;    /* [16] bf16, 4-byte aligned, or NULL                                  */
+    int32_t group;        /* 32, 64 or 128; divides h_in                                         */
+} lora_w4;
+
+/* Base product from 4-bit weights and adapter term, for any number of tokens:
+ *   y_i[c] = round(sum_k x_i[k] W[k][c] + scale_a * sum_{j<rank_a} t_i[j] B_a[j][c]),
+ *   t_i[j] = sum_k x_i[k] A_a[j][k],  a = ids[i],
+ * W as lora_w4 says.  x, ids, the adapters and y are as for lora_fused_gemm
+ * (y is written for every token; ids NULL: x W alone; a token whose id is -1,
+ * out of range or of an empty slot gets x_i W alone).  Products are of bf16 x
+ * and the exact v; sums, scales and the adapter term are fp32 (on the tiled
+ * path t is multiplied by B as two bf16 parts of 16 significand bits), and y
+ * is rounded once.  A non-finite value in a row of x makes that row's outputs
+ * non-finite.
+ * Short batches (decode) stream the weights' rows once per 64 tokens and run
+ * as one launch without ids, two with them, through `ws`
+ * (lora_fused_workspace_bytes); long ones run on tiles of 256 tokens.
+ * The pool must be bf16 and h_in / page_elems at most 32.
+ * Errors: ARG (null pointer, bad module, n_tokens < 0, a leading dimension
+ * below the width, misalignment, a group other than 32, 64, 128, both zero and
+ * table), DTYPE (pool not bf16), SHAPE (h_in not a multiple of the group, a
+ * leading dimension or batch past what the launch can address), WORKSPACE,
+ * HIP; nothing is launched on an argument error. */
+lora_status lora_fused_gemm_w4(const lora_pool *p, int32_t module,
+                               const void *x, int64_t ld_x, const lora_w4 *w,
+                               const int32_t *ids, int32_t n_tokens,
+                               void *y, int64_t ld_y,
+                               void *ws, size_t ws_bytes, void *stream);
+
+/* Gated feed-forward product with adapters on both projections:
+ *   g_i = x_i Wg + term of module_gate,  u_i = x_i Wu + term of module_up,
+ *   h_i[c] = round(act(g_i[c]) * u_i[c]),
+ * with the terms, ids and empty slots as for lora_fused_gemm.  g and u stay on
+ * chip (tiled path) or in fp32 (decode); h is rounded once.  The two modules
+ * have one h_in and one h_out.  x [n_tokens][ld_x] bf16 (16-byte aligned
+ * rows), w_gate and w_up [h_out][ld_w] bf16 (row c: the weights of output
+ * column c, 16-byte aligned rows), h [n_tokens][ld_h] bf16 (8-byte aligned
+ * rows), written for every token.  Any number of tokens; short batches and ws
+ * as for lora_fused_gemm_w4.  h is what a down projection takes as x.
+ * Errors: as lora_fused_gemm_w4, and ARG for an unknown act, SHAPE for modules
+ * of different widths. */
+typedef enum {
+    LORA_ACT_SILU = 0,       /* v / (1 + exp(-v))                                       */
+    LORA_ACT_GELU = 1,       /* v Phi(v), Phi the normal distribution function          */
+    LORA_ACT_GELU_TANH = 2   /* 0.5 v (1 + tanh(sqrt(2 / pi) (v + 0.044715 v^3)))       */
+} lora_act;
+lora_status lora_fused_glu(const lora_pool *p, int32_t module_gate, int32_t module_up,
+                           const void *x, int64_t ld_x, const void *w_gate, const void *w_up, int64_t ld_w,
+                           const int32_t *ids, int32_t n_tokens, lora_act act,
+                           void *h, int64_t ld_h,
+                           void *ws, size_t ws_bytes, void *stream);
+
+/* lora_fused_glu from FP8 base weights: w8_* [h_out][ld_w] OCP E4M3 codes
+ * (16-byte aligned, ld_w a multiple of 16) and scale_* [h_out] float32
+ * (16-byte aligned), both as for lora_fused_gemm_fp8w. */
+lora_status lora_fused_glu_fp8w(const lora_pool *p, int32_t module_gate, int32_t module_up,
+                                const void *x, int64_t ld_x, const void *w8_gate, const void *w8_up, int64_t ld_w,
+                                const float *scale_gate, const float *scale_up,
+                                const int32_t *ids, int32_t n_tokens, lora_act act,
+                                void *h, int64_t ld_h,
+                                void *ws, size_t ws_bytes, void *stream);
+
+/* lora_fused_glu from 4-bit base weights: both projections with one group, one
+ * ld_codes, and both with a table or both without (else SHAPE). */
+lora_status lora_fused_glu_w4(const lora_pool *p, int32_t module_gate, int32_t module_up,
+                              const void *x, int64_t ld_x, const lora_w4 *gate, const lora_w4 *up,
+                              const int32_t *ids, int32_t n_tokens, lora_act act,
+                              void *h, int64_t ld_h,
+                              void *ws, size_t ws_bytes, void *stream);
+
 /* ---- Adapter tiers: GPU slots <- host memory <- cold store ----------------
  * Study page "Multi-LoRA Serving", section "Memory: slots, tiers and paging"
  * and its cache simulation: the engine keeps a fixed number of adapters in

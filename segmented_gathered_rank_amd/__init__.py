@@ -22,6 +22,8 @@ __all__ = [
     "lora_segments_check", "lora_shrink_workspace_bytes", "lora_shrink", "lora_shrink_noalloc",
     "LORA_NOALLOC_SCRATCH_BYTES",
     "lora_expand", "lora_apply_sgmv", "lora_apply_sgmv_multi", "lora_x_run", "lora_apply_bgmv", "lora_apply_bgmv_ids", "lora_apply_bgmv_packed", "lora_fused_gemm", "lora_fused_gemm_fp8w",
+    "LORA_ACT_SILU", "LORA_ACT_GELU", "LORA_ACT_GELU_TANH", "lora_w4", "lora_w4_bind", "lora_fused_workspace_bytes",
+    "lora_fused_gemm_w4", "lora_fused_glu", "lora_fused_glu_fp8w", "lora_fused_glu_w4",
     "LORA_TIER_GPU", "LORA_TIER_HOST", "LORA_TIER_COLD", "lora_tiers_create", "lora_tiers_destroy",
     "lora_tiers_touch", "lora_tiers_stats", "lora_tiers_slot_of", "lora_tiers_acquire",
     "lora_tiers_batch_done", "lora_tiers_prefetch",
@@ -32,6 +34,7 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "liblora_mi3
 LORA_F32 = 0
 LORA_BF16 = 1
 LORA_MAX_RANK = 64
+LORA_ACT_SILU, LORA_ACT_GELU, LORA_ACT_GELU_TANH = 0, 1, 2
 LORA_NOALLOC_SCRATCH_BYTES = 16 * 1024 * 1024
 LORA_META_WORDS = 16
 META = {
@@ -69,6 +72,12 @@ class lora_segments(ctypes.Structure):
                 ("max_units", ctypes.c_int32), ("max_tiles", ctypes.c_int32), ("n_chunks", ctypes.c_int32)]
 
 
+class lora_w4(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("ld_codes", ctypes.c_int64), ("scale", ctypes.c_void_p),
+                ("zero", ctypes.c_void_p), ("ld_scale", ctypes.c_int64), ("table", ctypes.c_void_p),
+                ("group", ctypes.c_int32)]
+
+
 class lora_pool_stats_t(ctypes.Structure):
     _fields_ = [("n_pages", ctypes.c_int64), ("free_pages", ctypes.c_int64),
                 ("loaded_entries", ctypes.c_int32), ("loaded_slots", ctypes.c_int32),
@@ -77,6 +86,7 @@ class lora_pool_stats_t(ctypes.Structure):
 
 _P, _I32, _I64, _F, _SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t
 _SEGP = ctypes.POINTER(lora_segments)
+_W4P = ctypes.POINTER(lora_w4)
 _SIGS = {
     "lora_abi_version": (_I32, []),
     "lora_status_str": (ctypes.c_char_p, [_I32]),
@@ -105,6 +115,12 @@ _SIGS = {
     "lora_apply_bgmv_packed": (_I32, [_P, _I32, _I32, _P, _I64, _SEGP, _P, _I64, _I64, _I32, _P]),
     "lora_fused_gemm": (_I32, [_P, _I32, _P, _I64, _P, _I64, _P, _I32, _P, _I64, _P]),
     "lora_fused_gemm_fp8w": (_I32, [_P, _I32, _P, _I64, _P, _I64, _P, _P, _I32, _P, _I64, _P]),
+    "lora_fused_workspace_bytes": (_SZ, [_P, _I32, _I32, _I32]),
+    "lora_fused_gemm_w4": (_I32, [_P, _I32, _P, _I64, _W4P, _P, _I32, _P, _I64, _P, _SZ, _P]),
+    "lora_fused_glu": (_I32, [_P, _I32, _I32, _P, _I64, _P, _P, _I64, _P, _I32, _I32, _P, _I64, _P, _SZ, _P]),
+    "lora_fused_glu_fp8w": (_I32, [_P, _I32, _I32, _P, _I64, _P, _P, _I64, _P, _P, _P, _I32, _I32, _P, _I64, _P,
+                                   _SZ, _P]),
+    "lora_fused_glu_w4": (_I32, [_P, _I32, _I32, _P, _I64, _W4P, _W4P, _P, _I32, _I32, _P, _I64, _P, _SZ, _P]),
     "lora_tiers_create": (_I32, [ctypes.POINTER(_P), _I32, _I32]),
     "lora_tiers_destroy": (_I32, [_P]),
     "lora_tiers_touch": (_I32, [_P, _P, _I32, _P, _P, _P]),
@@ -313,6 +329,57 @@ def lora_fused_gemm_fp8w(pool: int, module: int, x, ld_x: int, w8, ld_w: int, w_
                          ld_y: int, stream=None) -> None:
     _check(_lib.lora_fused_gemm_fp8w(pool, module, _ptr(x), ld_x, _ptr(w8), ld_w, _ptr(w_scale), _ptr(ids),
                                      n_tokens, _ptr(y), ld_y, _stream(stream)), "lora_fused_gemm_fp8w")
+
+
+def lora_w4_bind(codes, scale, group: int, zero=None, table=None) -> lora_w4:
+    """4-bit weights of one projection from its device tensors (codes [h_out][ld] uint8, scale
+    and zero [h_in / group][ld]; rows dense); the returned struct keeps them alive."""
+    for t in (codes, scale, zero, table):
+        if t is not None and t.stride(-1) != 1:
+            raise ValueError("the rows of codes, scale, zero and table must be dense")
+    if zero is not None and zero.stride(0) != scale.stride(0):
+        raise ValueError("zero and scale need one row stride")
+    w = lora_w4(_ptr(codes), codes.stride(0), _ptr(scale), _ptr(zero), scale.stride(0), _ptr(table), group)
+    w._keep = (codes, scale, zero, table)
+    return w
+
+
+def _ws_bytes(ws, ws_bytes: int) -> int:
+    if ws is not None and ws_bytes == 0 and hasattr(ws, "numel"):
+        return ws.numel() * ws.element_size()
+    return ws_bytes
+
+
+def lora_fused_workspace_bytes(pool: int, module: int, n_proj: int, n_tokens: int) -> int:
+    return int(_lib.lora_fused_workspace_bytes(pool, module, n_proj, n_tokens))
+
+
+def lora_fused_gemm_w4(pool: int, module: int, x, ld_x: int, w: lora_w4, ids, n_tokens: int, y, ld_y: int, ws=None,
+                       ws_bytes: int = 0, stream=None) -> None:
+    _check(_lib.lora_fused_gemm_w4(pool, module, _ptr(x), ld_x, ctypes.byref(w), _ptr(ids), n_tokens, _ptr(y), ld_y,
+                                   _ptr(ws), _ws_bytes(ws, ws_bytes), _stream(stream)), "lora_fused_gemm_w4")
+
+
+def lora_fused_glu(pool: int, module_gate: int, module_up: int, x, ld_x: int, w_gate, w_up, ld_w: int, ids,
+                   n_tokens: int, act: int, h, ld_h: int, ws=None, ws_bytes: int = 0, stream=None) -> None:
+    _check(_lib.lora_fused_glu(pool, module_gate, module_up, _ptr(x), ld_x, _ptr(w_gate), _ptr(w_up), ld_w,
+                               _ptr(ids), n_tokens, act, _ptr(h), ld_h, _ptr(ws), _ws_bytes(ws, ws_bytes),
+                               _stream(stream)), "lora_fused_glu")
+
+
+def lora_fused_glu_fp8w(pool: int, module_gate: int, module_up: int, x, ld_x: int, w8_gate, w8_up, ld_w: int,
+                        scale_gate, scale_up, ids, n_tokens: int, act: int, h, ld_h: int, ws=None, ws_bytes: int = 0,
+                        stream=None) -> None:
+    _check(_lib.lora_fused_glu_fp8w(pool, module_gate, module_up, _ptr(x), ld_x, _ptr(w8_gate), _ptr(w8_up), ld_w,
+                                    _ptr(scale_gate), _ptr(scale_up), _ptr(ids), n_tokens, act, _ptr(h), ld_h,
+                                    _ptr(ws), _ws_bytes(ws, ws_bytes), _stream(stream)), "lora_fused_glu_fp8w")
+
+
+def lora_fused_glu_w4(pool: int, module_gate: int, module_up: int, x, ld_x: int, gate: lora_w4, up: lora_w4, ids,
+                      n_tokens: int, act: int, h, ld_h: int, ws=None, ws_bytes: int = 0, stream=None) -> None:
+    _check(_lib.lora_fused_glu_w4(pool, module_gate, module_up, _ptr(x), ld_x, ctypes.byref(gate), ctypes.byref(up),
+                                  _ptr(ids), n_tokens, act, _ptr(h), ld_h, _ptr(ws), _ws_bytes(ws, ws_bytes),
+                                  _stream(stream)), "lora_fused_glu_w4")
 
 
 # ------------------------------------------------------------------ adapter tiers

@@ -694,18 +694,17 @@ lora_status fused_call(const lora_pool* p, int32_t module, const void* x, int64_
   FusedArgs fa{};
   fa.pv = p->view();
   fa.x = static_cast<const __bf16*>(x);
-  fa.w = static_cast<const __bf16*>(w);
-  fa.w8 = w8;
-  fa.w_scale = w_scale;
+  fa.w[0].w = w8 ? static_cast<const void*>(w8) : w;
+  fa.w[0].scale = w_scale;
   fa.ids = ids;
   fa.y = static_cast<__bf16*>(y);
   fa.ld_x = ld_x;
-  fa.ld_w = ld_w;
+  fa.ld_w = w8 ? ld_w : 2 * ld_w;
   fa.ld_y = ld_y;
   fa.n = n_tokens;
   fa.h_in = static_cast<int32_t>(h_in);
   fa.h_out = static_cast<int32_t>(h_out);
-  fa.module = module;
+  fa.module[0] = module;
   const int64_t n_rt = (static_cast<int64_t>(n_tokens) + kFgBM - 1) / kFgBM;
   fa.n_ct = static_cast<int32_t>((h_out + kFgBN - 1) / kFgBN);
   const int64_t tiles = n_rt * fa.n_ct;
@@ -715,14 +714,14 @@ lora_status fused_call(const lora_pool* p, int32_t module, const void* x, int64_
   hipStream_t s = static_cast<hipStream_t>(stream);
   if (w8) {
     if (ids)
-      hipLaunchKernelGGL((k_fused_gemm<true, true>), dim3(grid), dim3(kFgThreads), 0, s, fa);
+      hipLaunchKernelGGL((k_fused_gemm<true, WKind::kFp8>), dim3(grid), dim3(kFgThreads), 0, s, fa);
     else
-      hipLaunchKernelGGL((k_fused_gemm<false, true>), dim3(grid), dim3(kFgThreads), 0, s, fa);
+      hipLaunchKernelGGL((k_fused_gemm<false, WKind::kFp8>), dim3(grid), dim3(kFgThreads), 0, s, fa);
   } else {
     if (ids)
-      hipLaunchKernelGGL((k_fused_gemm<true, false>), dim3(grid), dim3(kFgThreads), 0, s, fa);
+      hipLaunchKernelGGL((k_fused_gemm<true, WKind::kBf16>), dim3(grid), dim3(kFgThreads), 0, s, fa);
     else
-      hipLaunchKernelGGL((k_fused_gemm<false, false>), dim3(grid), dim3(kFgThreads), 0, s, fa);
+      hipLaunchKernelGGL((k_fused_gemm<false, WKind::kBf16>), dim3(grid), dim3(kFgThreads), 0, s, fa);
   }
   return hipGetLastError() == hipSuccess ? LORA_OK : LORA_ERR_HIP;
 }

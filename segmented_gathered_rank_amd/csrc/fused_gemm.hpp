@@ -31,12 +31,27 @@
 // of each unit's adapter, scaled, split into two bf16 parts (hi + lo carry 16
 // significand bits) and multiplied by B on the same MFMA shape into the base
 // accumulators.  Rows an adapter does not have read the pool's zero page.
+//
+// Gated pass (GLU): h = act(x Wg + term) * (x Wu + term).  A tile is 256 tokens
+// x 128 output columns of both projections: of a wave's four 16-column blocks
+// two are gate columns and two are the up columns of the same outputs, so the
+// activation and the product happen on the lane's own accumulators and only h
+// is written.  An adapter's units are those of its two modules; a unit's B rows
+// are zero in the other projection's blocks.
+//
+// 4-bit codes.  A weight s (q - z) has up to 13 significand bits, so rounding
+// it to bf16 on the way into LDS would add an error of the size of y's own
+// rounding.  Instead LDS holds the exact integers q - z (or the codebook's
+// values), the MFMAs of one 64-k step (32 for groups of 32) start from zero,
+// and their sum is added to the accumulators times the group's scale in fp32:
+// one vector FMA per accumulator and step, next to two MFMAs of 16 clocks per
+// four of them.
 #pragma once
 
 #include <type_traits>
 
+#include "base_args.hpp"
 #include "common.hpp"
-#include "mfma_kernels.hpp"   // bf16x8
 
 namespace lora {
 
@@ -50,7 +65,8 @@ constexpr int kFgPassUnits = 2;   // 16-rank units per pass over K, at most
 constexpr int kFgMaxPpr = 32;     // A pages per rank row (h_in / page_elems) at most
 constexpr int kFgMaxBpages = 8;   // B pages a tile's 256 columns touch, at most (page >= 64)
 constexpr int kFgMaxSlots = 8192; // slot ids a tile's bitmap covers
-constexpr int kFgMaxUnits = kFgBM * 4;   // 256 distinct adapters x 4 units (rank 64)
+constexpr int kFgMaxUnits = kFgBM * 4;   // 256 distinct adapters x 4 units (rank 64), per projection
+constexpr int kFgGluCols = kFgBN / 2;    // output columns per tile of a gated pass
 constexpr int kFgTRow = 144;      // bytes per token row of the t exchange (128 + 16: no bank conflicts)
 constexpr int kFgBOff = 16384;    // B rows in the idle stage buffer's second half, after T
 
@@ -61,13 +77,14 @@ constexpr int kFgBOff = 16384;    // B rows in the idle stage buffer's second ha
 struct FusedArgs {
   PoolView pv;
   const __bf16* x;        // [n][ld_x]
-  const __bf16* w;        // W^T: [h_out][ld_w], row c = weights of output column c
-  const uint8_t* w8;      // W8 kernel: W^T as OCP e4m3 codes, [h_out][ld_w] bytes
-  const float* w_scale;   // W8 kernel: [h_out] scale of each output column
+  WView w[2];             // W^T of the projection, or of gate and up: row c = weights of output column c
   const int32_t* ids;     // [n]; unused by the base-only kernel
   __bf16* y;              // [n][ld_y], written
-  int64_t ld_x, ld_w, ld_y;
-  int32_t n, h_in, h_out, module;
+  int64_t ld_x, ld_w, ld_y;   // ld_w in bytes
+  int32_t n, h_in, h_out;
+  int32_t module[2];
+  int32_t act;            // gated pass: lora_act
+  int32_t group_shift;    // 4-bit: log2(group / 32)
   int32_t n_ct;           // column tiles
   int32_t n_tiles;        // row tiles x column tiles
 };
@@ -92,6 +109,17 @@ __device__ __forceinline__ lds_ptr_t fg_lds_ptr(void* p) {
   return reinterpret_cast<lds_ptr_t>(reinterpret_cast<uintptr_t>(p));
 }
 
+// Each lane's 16 bytes at `from` to LDS at the wave's `to` + 16 * lane.  (A
+// function of its own: the builtin's size is checked against the target, which
+// fails silently for a dependent expression in the host's pass.)
+__device__ __forceinline__ void fg_load16(const void* from, void* to) {
+  __builtin_amdgcn_global_load_lds(from, fg_lds_ptr(to), 16, 0, 0);
+}
+
+// Projections of one pass.
+constexpr int fg_np(bool glu) { return glu ? 2 : 1; }
+
+template <bool GLU, bool W4>
 struct FgShared {
   // two pipeline stages of [256][64] bf16 x and W^T tiles; after a pass the
   // idle one holds t (first half) and the units' B rows (second half)
@@ -100,13 +128,12 @@ struct FgShared {
   int32_t ids[kFgBM];
   uint32_t bitmap[kFgMaxSlots / 32];
   int32_t dslot[kFgBM];            // distinct adapters of the tile, ascending
-  int32_t drank[kFgBM];
-  float dscale[kFgBM];
-  int32_t da_off[kFgBM], db_off[kFgBM];
-  int32_t unit[kFgMaxUnits];       // (distinct index << 2) | unit of 16 ranks
+  SlotEntry dent[fg_np(GLU)][kFgBM];           // their entries
+  uint16_t unit[fg_np(GLU) * kFgMaxUnits];     // (distinct index << 3) | (projection << 2) | unit of 16 ranks
   int32_t pid[kFgPassUnits][16][kFgMaxPpr];        // A pages of the pass's units
   int32_t bpid[kFgPassUnits][16][kFgMaxBpages];    // B pages of the pass's units over the tile's columns
   int32_t wsum[kFgWaves];
+  alignas(8) uint16_t wscale[W4 ? 2 : 1][W4 ? 2 : 1][W4 ? kFgBN : 1];   // 4-bit: scales of a stage's two half steps
 };
 
 // Exclusive prefix sum over the workgroup's threads; returns the total in *total.
@@ -149,13 +176,16 @@ __device__ __forceinline__ uint32_t fg_e4m3x2_to_bf16x2(uint32_t w, bool high) {
   return __builtin_bit_cast(uint32_t, v);
 }
 
-// LORA false: base product only.  W8: W^T given as e4m3 codes with a scale per
-// output column (W8A16: the codes are widened to bf16 on their way into LDS,
-// exactly, and the column scale multiplies the base product before the
-// adapter term is added).
-template <bool LORA, bool W8>
+// LORA false: base product only.  WK: storage of W^T.  kFp8: e4m3 codes with a
+// scale per output column (W8A16: the codes are widened to bf16 on their way
+// into LDS, exactly, and the column scale multiplies the base product before
+// the adapter term is added).  G32: 4-bit groups of 32 (else 64 or more).
+template <bool LORA, WKind WK, bool GLU = false, bool G32 = false>
 __global__ __launch_bounds__(kFgThreads, 1) void k_fused_gemm(FusedArgs a) {
-  __shared__ FgShared sh;
+  constexpr bool W8 = WK == WKind::kFp8, W4 = is_w4(WK);
+  constexpr int NP = fg_np(GLU);
+  constexpr int TC = GLU ? kFgGluCols : kFgBN;   // output columns per tile
+  __shared__ FgShared<GLU, W4> sh;
   constexpr int CB = 4;   // 16-column blocks per wave
   constexpr int SB = 2;   // 16-token shrink blocks per wave
   const int tid = threadIdx.x, lane = tid & 63;
@@ -169,7 +199,7 @@ __global__ __launch_bounds__(kFgThreads, 1) void k_fused_gemm(FusedArgs a) {
   const int tile = (blockIdx.x & 7) * per_xcd + (blockIdx.x >> 3);
   if (tile >= a.n_tiles) return;
   const int rt = tile / a.n_ct, ct = tile - rt * a.n_ct;
-  const int row0 = rt * kFgBM, col0 = ct * kFgBN;
+  const int row0 = rt * kFgBM, col0 = ct * TC;
   const int nk = a.h_in / kFgBK;
 
   // ---- staging: per K step each wave moves 4 blocks of 8 rows x 128 B of
@@ -179,37 +209,41 @@ __global__ __launch_bounds__(kFgThreads, 1) void k_fused_gemm(FusedArgs a) {
   // past the end repeat the last row (their results are never stored).
   const int lr = lane >> 3;
   const char* xbase = reinterpret_cast<const char*>(a.x + static_cast<int64_t>(row0) * a.ld_x);
-  const char* wbase = reinterpret_cast<const char*>(a.w + static_cast<int64_t>(col0) * a.ld_w);
+  // row r of the W^T tile is output column col0 + wcol(r) of projection wproj(r):
+  // in a gated pass the rows alternate between 32 gate and 32 up columns
+  auto wproj = [](int r) { return GLU ? (r >> 5) & 1 : 0; };
+  auto wcol = [](int r) { return GLU ? ((r >> 6) << 5) + (r & 31) : r; };
+  const char* wbase = static_cast<const char*>(a.w[wproj(8 * wave)].w) + static_cast<int64_t>(col0) * a.ld_w;
   uint32_t xoff[4], woff[4];
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
     const int r = 8 * (wave + 8 * q) + lr;
     const int lc = (lane & 7) ^ fg_swz_key(r);
     xoff[q] = static_cast<uint32_t>((min(r, a.n - 1 - row0) * a.ld_x + 8 * lc) * 2);
-    woff[q] = static_cast<uint32_t>((min(r, a.h_out - 1 - col0) * a.ld_w + 8 * lc) * 2);
+    woff[q] = static_cast<uint32_t>(min(wcol(r), a.h_out - 1 - col0) * a.ld_w + 16 * lc);
   }
   auto load_x = [&](int kt, int buf) {
     const char* xb = xbase + kt * (kFgBK * 2);
 #pragma unroll
     for (int q = 0; q < 4; ++q)
-      __builtin_amdgcn_global_load_lds(xb + xoff[q], fg_lds_ptr(sh.stage[buf][0] + 1024 * (wave + 8 * q)), 16, 0, 0);
+      fg_load16(xb + xoff[q], sh.stage[buf][0] + 1024 * (wave + 8 * q));
   };
   auto load_w = [&](int kt, int buf) {
     const char* wb = wbase + kt * (kFgBK * 2);
 #pragma unroll
     for (int q = 0; q < 4; ++q)
-      __builtin_amdgcn_global_load_lds(wb + woff[q], fg_lds_ptr(sh.stage[buf][1] + 1024 * (wave + 8 * q)), 16, 0, 0);
+      fg_load16(wb + woff[q], sh.stage[buf][1] + 1024 * (wave + 8 * q));
   };
   // W8: each thread moves two 16-byte pieces of e4m3 codes per K step (rows
   // i / 4 of the tile, k 16 (i % 4) .. +16, for i = tid, tid + 512) through
   // registers, widened to four bf16 chunks in the same swizzled layout
-  const uint8_t* w8base = W8 ? a.w8 + static_cast<int64_t>(col0) * a.ld_w : nullptr;
+  const uint8_t* w8base = static_cast<const uint8_t*>(a.w[wproj(16 * wave)].w) + static_cast<int64_t>(col0) * a.ld_w;
   uint32_t w8off[2];
 #pragma unroll
   for (int q = 0; q < 2; ++q) {
     const int i = tid + kFgThreads * q;
     const int r = i >> 2;
-    w8off[q] = static_cast<uint32_t>(min(r, a.h_out - 1 - col0) * a.ld_w + 16 * (i & 3));
+    w8off[q] = static_cast<uint32_t>(min(wcol(r), a.h_out - 1 - col0) * a.ld_w + 16 * (i & 3));
   }
   u32x4 w8reg[2];
   auto issue_w8 = [&](int kt) {
@@ -231,8 +265,45 @@ __global__ __launch_bounds__(kFgThreads, 1) void k_fused_gemm(FusedArgs a) {
       *reinterpret_cast<u32x4*>(Ws + fg_swz(r, c + 1)) = hi;
     }
   };
+  // 4-bit: each thread moves one 16-byte piece of codes per K step (32 k of row
+  // tid / 2) through registers, with its scale and zero point, and writes four
+  // bf16 chunks in the same swizzled layout
+  const int r4 = tid >> 1, half4 = tid & 1;
+  const WView& wv4 = a.w[wproj(32 * wave)];
+  const int col4 = col0 + min(wcol(r4), a.h_out - 1 - col0);
+  const uint8_t* w4base = static_cast<const uint8_t*>(wv4.w) + static_cast<int64_t>(col4) * a.ld_w + 16 * half4;
+  u32x4 w4reg;
+  uint16_t w4s = 0;
+  uint8_t w4z = 8;
+  W4Table w4tab;
+  if constexpr (WK == WKind::kTable4) w4tab.load(wv4.table);
+  auto issue_w4 = [&](int kt) {
+    w4reg = *reinterpret_cast<const u32x4*>(w4base + kt * (kFgBK / 2));
+    const int64_t o = static_cast<int64_t>((2 * kt + half4) >> a.group_shift) * wv4.ld_scale + col4;
+    w4s = static_cast<const uint16_t*>(wv4.scale)[o];
+    if (WK == WKind::kInt4 && wv4.zero) w4z = wv4.zero[o];
+  };
+  auto store_w4 = [&](int buf) {
+    if constexpr (W4) {
+      unsigned char* Ws = sh.stage[buf][1];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        bf16x8 v;
+        if constexpr (WK == WKind::kTable4) {
+          v = w4_widen<WK>(w4reg[j], w4tab);
+        } else {
+          v = w4_minus(w4reg[j], static_cast<float>(w4z));
+        }
+        *reinterpret_cast<bf16x8*>(Ws + fg_swz(r4, 4 * half4 + j)) = v;
+      }
+      sh.wscale[buf][half4][r4] = w4s;
+    }
+  };
   load_x(0, 0);
-  if constexpr (W8) {
+  if constexpr (W4) {
+    issue_w4(0);
+    store_w4(0);
+  } else if constexpr (W8) {
     issue_w8(0);
     store_w8(0);
   } else {
@@ -259,17 +330,21 @@ __global__ __launch_bounds__(kFgThreads, 1) void k_fused_gemm(FusedArgs a) {
     for (uint32_t w = word; w; w &= w - 1) sh.dslot[off++] = tid * 32 + __ffs(w) - 1;
     if (tid < kFgBM) sh.ids[tid] = id;
     __syncthreads();
-    int nu = 0;
+    int nu[NP] = {};
+    int nus = 0;
     if (tid < n_dist) {
-      const SlotEntry e = a.pv.entries[static_cast<int64_t>(sh.dslot[tid]) * a.pv.n_modules + a.module];
-      sh.drank[tid] = e.rank;
-      sh.dscale[tid] = e.scale;
-      sh.da_off[tid] = e.a_off;
-      sh.db_off[tid] = e.b_off;
-      nu = (max(e.rank, 0) + 15) >> 4;
+#pragma unroll
+      for (int p = 0; p < NP; ++p) {
+        const SlotEntry e = a.pv.entries[static_cast<int64_t>(sh.dslot[tid]) * a.pv.n_modules + a.module[p]];
+        sh.dent[p][tid] = e;
+        nu[p] = (max(e.rank, 0) + 15) >> 4;
+        nus += nu[p];
+      }
     }
-    int uoff = fg_block_scan(nu, sh.wsum, &n_units);
-    for (int j = 0; j < nu; ++j) sh.unit[uoff + j] = (tid << 2) | j;
+    int uoff = fg_block_scan(nus, sh.wsum, &n_units);
+#pragma unroll
+    for (int p = 0; p < NP; ++p)
+      for (int j = 0; j < nu[p]; ++j) sh.unit[uoff++] = static_cast<uint16_t>((tid << 3) | (p << 2) | j);
     __syncthreads();
   }
 
@@ -286,19 +361,20 @@ __global__ __launch_bounds__(kFgThreads, 1) void k_fused_gemm(FusedArgs a) {
     for (int i = tid; i < na; i += kFgThreads) {
       const int u = i / (16 * ppr_a), rest = i - u * 16 * ppr_a;
       const int jr = rest / ppr_a, kp = rest - jr * ppr_a;
-      const int un = sh.unit[u0 + u], d = un >> 2;
+      const int un = sh.unit[u0 + u];
+      const SlotEntry& e = sh.dent[(un >> 2) & (NP - 1)][un >> 3];
       const int jj = ((un & 3) << 4) + jr;
-      sh.pid[u][jr][kp] = jj < sh.drank[d] ? a.pv.page_ids[sh.da_off[d] + jj * ppr_a + kp] : a.pv.zero_page;
+      sh.pid[u][jr][kp] = jj < e.rank ? a.pv.page_ids[e.a_off + jj * ppr_a + kp] : a.pv.zero_page;
     }
-    const int ncp = (min(col0 + kFgBN, a.h_out) - 1) / h - cp0 + 1;
+    const int ncp = (min(col0 + TC, a.h_out) - 1) / h - cp0 + 1;
     const int nb = np * 16 * ncp;
     for (int i = tid; i < nb; i += kFgThreads) {
       const int u = i / (16 * ncp), rest = i - u * 16 * ncp;
       const int jr = rest / ncp, ci = rest - jr * ncp;
-      const int un = sh.unit[u0 + u], d = un >> 2;
+      const int un = sh.unit[u0 + u];
+      const SlotEntry& e = sh.dent[(un >> 2) & (NP - 1)][un >> 3];
       const int jj = ((un & 3) << 4) + jr;
-      sh.bpid[u][jr][ci] =
-          jj < sh.drank[d] ? a.pv.page_ids[sh.db_off[d] + jj * ppr_b + cp0 + ci] : a.pv.zero_page;
+      sh.bpid[u][jr][ci] = jj < e.rank ? a.pv.page_ids[e.b_off + jj * ppr_b + cp0 + ci] : a.pv.zero_page;
     }
   };
   // A rows of the pass's P units into astage: waves 0 .. 2P - 1 move one
@@ -312,25 +388,25 @@ __global__ __launch_bounds__(kFgThreads, 1) void k_fused_gemm(FusedArgs a) {
       const int kp = ppr_a == 1 ? 0 : k0 / h;
       const int pid = sh.pid[arow >> 4][arow & 15][kp];
       const __bf16* src = pages + static_cast<int64_t>(pid) * h + (k0 - kp * h) + 8 * alc;
-      __builtin_amdgcn_global_load_lds(src, fg_lds_ptr(sh.astage[buf] + 1024 * wave), 16, 0, 0);
+      fg_load16(src, sh.astage[buf] + 1024 * wave);
     }
   };
-  // B rows of the pass's P units for the tile's columns into dst:
-  // [u][rank row][256 columns] bf16, 1 KB blocks of two rank rows; columns
-  // past h_out read the zero page
-  auto load_b = [&](auto P_, unsigned char* dst) {
+  // B rows of the pass's P units (the first is u0) for the tile's columns into
+  // dst: [u][rank row][256 W^T rows] bf16, 1 KB blocks of two rank rows; columns
+  // past h_out and the other projection's read the zero page
+  auto load_b = [&](auto P_, int u0, unsigned char* dst) {
     constexpr int P = decltype(P_)::value;
-    const int col = col0 + 8 * (lane & 31);
-    const bool in = col < a.h_out;
-    const int cp = in ? col / h : cp0;
-    const int cin = in ? col - cp * h : 0;
+    const int col = col0 + wcol(8 * (lane & 31));
+    const bool in_out = col < a.h_out;
+    const int cp = in_out ? col / h : cp0;
+    const int cin = in_out ? col - cp * h : 0;
 #pragma unroll
     for (int q = 0; q < P; ++q) {
       const int b = wave + kFgWaves * q;   // block: unit b / 8, rank rows 2 (b % 8) .. +2
       const int jr = 2 * (b & 7) + (lane >> 5);
+      const bool in = in_out && (!GLU || ((sh.unit[u0 + q] >> 2) & 1) == wproj(8 * (lane & 31)));
       const int pid = in ? sh.bpid[b >> 3][jr][cp - cp0] : a.pv.zero_page;
-      __builtin_amdgcn_global_load_lds(pages + static_cast<int64_t>(pid) * h + cin,
-                                       fg_lds_ptr(dst + 1024 * b), 16, 0, 0);
+      fg_load16(pages + static_cast<int64_t>(pid) * h + cin, dst + 1024 * b);
     }
   };
 
@@ -347,10 +423,71 @@ __global__ __launch_bounds__(kFgThreads, 1) void k_fused_gemm(FusedArgs a) {
   const int srow = 128 * wm + 32 * wn + l16;   // x rows of this wave's shrink tokens: + 16 i
   unsigned char* const idle = sh.stage[nk & 1][0];   // the buffer no step of a pass's last one reads
 
+  // One K step of the base product from 4-bit codes: the step's sums start
+  // from zero and join the accumulators times their group's scale.
+  auto step_w4 = [&](auto P_, int buf) {
+    constexpr int P = decltype(P_)::value;
+    if constexpr (W4) {
+      const unsigned char* Xs = sh.stage[buf][0];
+      const unsigned char* Ws = sh.stage[buf][1];
+      bf16x8 wf[2][CB];
+      f32x4 sc[G32 ? 2 : 1][CB];
+#pragma unroll
+      for (int cb = 0; cb < CB; ++cb) {
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) wf[ks][cb] = fg_lds8(Ws, fg_swz(wrow + 16 * cb, 4 * ks + lq));
+#pragma unroll
+        for (int g = 0; g < (G32 ? 2 : 1); ++g) {
+          const u32x2 v = *reinterpret_cast<const u32x2*>(&sh.wscale[buf][g][64 * wn + 16 * cb + 4 * lq]);
+          sc[g][cb] = f32x4{bf16lo(v.x), bf16hi(v.x), bf16lo(v.y), bf16hi(v.y)};
+        }
+      }
+      const f32x4 none{0.f, 0.f, 0.f, 0.f};
+      bf16x8 xs[2][SB];
+#pragma unroll
+      for (int tb = 0; tb < 8; ++tb) {
+        bf16x8 xf[2];
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) xf[ks] = fg_lds8(Xs, fg_swz(xrow + 16 * tb, 4 * ks + lq));
+        f32x4 sum[CB];
+#pragma unroll
+        for (int cb = 0; cb < CB; ++cb)
+          sum[cb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf[0][cb], xf[0], none, 0, 0, 0);
+        if constexpr (G32) {
+#pragma unroll
+          for (int cb = 0; cb < CB; ++cb) acc[cb][tb] += sc[0][cb] * sum[cb];
+        }
+#pragma unroll
+        for (int cb = 0; cb < CB; ++cb)
+          sum[cb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf[1][cb], xf[1], G32 ? none : sum[cb], 0, 0, 0);
+#pragma unroll
+        for (int cb = 0; cb < CB; ++cb) acc[cb][tb] += sc[G32 ? 1 : 0][cb] * sum[cb];
+        if constexpr (P > 0) {
+#pragma unroll
+          for (int ks = 0; ks < 2; ++ks) {
+            if (tb < SB) xs[ks][tb] = xf[ks];
+            else xs[ks][tb % SB] = tb / SB == wn ? xf[ks] : xs[ks][tb % SB];
+          }
+        }
+      }
+      if constexpr (P > 0) {
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+          for (int u = 0; u < P; ++u) {
+            const bf16x8 af = fg_lds8(sh.astage[buf], fg_swz(16 * u + l16, 4 * ks + lq));
+#pragma unroll
+            for (int i = 0; i < SB; ++i)
+              tacc[i][u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(af, xs[ks][i], tacc[i][u], 0, 0, 0);
+          }
+      }
+    }
+  };
+
   // One pass over K.  BASE: the base product with the shrink of P units
   // riding along; otherwise the shrink alone.  During the last step the P
   // units' B rows go to the idle buffer.
-  auto kloop = [&](auto P_, auto BASE_) {
+  auto kloop = [&](auto P_, auto BASE_, int u0) {
     constexpr int P = decltype(P_)::value;
     constexpr bool BASE = decltype(BASE_)::value != 0;
 #pragma unroll
@@ -360,6 +497,10 @@ __global__ __launch_bounds__(kFgThreads, 1) void k_fused_gemm(FusedArgs a) {
     auto step = [&](int buf) {
       const unsigned char* Xs = sh.stage[buf][0];
       const unsigned char* Ws = sh.stage[buf][1];
+      if constexpr (BASE && W4) {
+        step_w4(P_, buf);
+        return;
+      }
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks) {
         const int c = 4 * ks + lq;
@@ -399,14 +540,16 @@ __global__ __launch_bounds__(kFgThreads, 1) void k_fused_gemm(FusedArgs a) {
     for (int kt = 0; kt < nk - 1; ++kt) {
       const int buf = kt & 1;
       load_x(kt + 1, buf ^ 1);   // that buffer's readers passed the last barrier
-      if constexpr (BASE && !W8) load_w(kt + 1, buf ^ 1);
+      if constexpr (BASE && !W8 && !W4) load_w(kt + 1, buf ^ 1);
       if constexpr (BASE && W8) issue_w8(kt + 1);
+      if constexpr (BASE && W4) issue_w4(kt + 1);
       if constexpr (P > 0) load_a(P_, kt + 1, buf ^ 1);
       step(buf);
       if constexpr (BASE && W8) store_w8(buf ^ 1);   // widened after this step's reads of buf
+      if constexpr (BASE && W4) store_w4(buf ^ 1);
       __syncthreads();
     }
-    if constexpr (P > 0) load_b(P_, idle + kFgTileBytes + kFgBOff);
+    if constexpr (P > 0) load_b(P_, u0, idle + kFgTileBytes + kFgBOff);
     step((nk - 1) & 1);
     __syncthreads();   // also: the B rows have landed
   };
@@ -424,12 +567,13 @@ __global__ __launch_bounds__(kFgThreads, 1) void k_fused_gemm(FusedArgs a) {
       const int id = sh.ids[tok];
 #pragma unroll
       for (int u = 0; u < P; ++u) {
-        const int un = sh.unit[u0 + u], d = un >> 2;
+        const int un = sh.unit[u0 + u], d = un >> 3;
         float s = 0.f;
         int rows = 0;
         if (sh.dslot[d] == id) {
-          s = sh.dscale[d];
-          rows = sh.drank[d] - ((un & 3) << 4);
+          const SlotEntry& e = sh.dent[(un >> 2) & (NP - 1)][d];
+          s = e.scale;
+          rows = e.rank - ((un & 3) << 4);
         }
         __bf16 hi[4], lo[4];
 #pragma unroll
@@ -466,14 +610,17 @@ __global__ __launch_bounds__(kFgThreads, 1) void k_fused_gemm(FusedArgs a) {
     }
   };
 
+  // Output column of this lane's accumulators of block cb: + 0 .. 3.
+  auto out_col = [&](int cb) { return col0 + (GLU ? 32 * wn + 16 * (cb & 1) : 64 * wn + 16 * cb) + 4 * lq; };
   // W8: the base accumulators times each output column's scale (before any
-  // adapter term is added).  Lane: columns col0 + 64 wn + 16 cb + 4 lq .. +4.
+  // adapter term is added).
   auto scale_base = [&]() {
     if constexpr (W8) {
 #pragma unroll
       for (int cb = 0; cb < CB; ++cb) {
-        const int col = col0 + 64 * wn + 16 * cb + 4 * lq;
-        const f32x4 sc = col < a.h_out ? *reinterpret_cast<const f32x4*>(a.w_scale + col) : f32x4{0.f, 0.f, 0.f, 0.f};
+        const int col = out_col(cb);
+        const float* ws = static_cast<const float*>(a.w[GLU ? cb >> 1 : 0].scale);
+        const f32x4 sc = col < a.h_out ? *reinterpret_cast<const f32x4*>(ws + col) : f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int tb = 0; tb < 8; ++tb) acc[cb][tb] *= sc;
       }
@@ -490,18 +637,18 @@ __global__ __launch_bounds__(kFgThreads, 1) void k_fused_gemm(FusedArgs a) {
     if (np0 == 2) {
       load_a(fg_int<2>{}, 0, 0);
       __syncthreads();
-      kloop(fg_int<2>{}, fg_int<1>{});
+      kloop(fg_int<2>{}, fg_int<1>{}, 0);
       scale_base();
       expand(fg_int<2>{}, 0);
     } else if (np0 == 1) {
       load_a(fg_int<1>{}, 0, 0);
       __syncthreads();
-      kloop(fg_int<1>{}, fg_int<1>{});
+      kloop(fg_int<1>{}, fg_int<1>{}, 0);
       scale_base();
       expand(fg_int<1>{}, 0);
     } else {
       __syncthreads();
-      kloop(fg_int<0>{}, fg_int<1>{});
+      kloop(fg_int<0>{}, fg_int<1>{}, 0);
       scale_base();
     }
     // ---- further passes, one unit at a time, shrink only
@@ -512,12 +659,12 @@ __global__ __launch_bounds__(kFgThreads, 1) void k_fused_gemm(FusedArgs a) {
       load_x(0, 0);
       load_a(fg_int<1>{}, 0, 0);
       __syncthreads();
-      kloop(fg_int<1>{}, fg_int<0>{});
+      kloop(fg_int<1>{}, fg_int<0>{}, u0);
       expand(fg_int<1>{}, u0);
     }
   } else {
     __syncthreads();   // stage 0 has landed (the barrier waits for the loads)
-    kloop(fg_int<0>{}, fg_int<1>{});
+    kloop(fg_int<0>{}, fg_int<1>{}, 0);
     scale_base();
   }
 
@@ -529,12 +676,15 @@ __global__ __launch_bounds__(kFgThreads, 1) void k_fused_gemm(FusedArgs a) {
     if (tok >= a.n) continue;
     __bf16* yr = a.y + static_cast<int64_t>(tok) * a.ld_y;
 #pragma unroll
-    for (int cb = 0; cb < CB; ++cb) {
-      const int col = col0 + 64 * wn + 16 * cb + 4 * lq;
+    for (int cb = 0; cb < (GLU ? CB / 2 : CB); ++cb) {
+      const int col = out_col(cb);
       if (col >= a.h_out) continue;
       __bf16 o[4];
 #pragma unroll
-      for (int v = 0; v < 4; ++v) o[v] = static_cast<__bf16>(acc[cb][tb][v]);
+      for (int v = 0; v < 4; ++v) {
+        if constexpr (GLU) o[v] = static_cast<__bf16>(glu_act(a.act, acc[cb][tb][v]) * acc[cb + CB / 2][tb][v]);
+        else o[v] = static_cast<__bf16>(acc[cb][tb][v]);
+      }
       *reinterpret_cast<u32x2*>(yr + col) = __builtin_bit_cast(u32x2, o);
     }
   }

@@ -1,0 +1,62 @@
+// Launches of the tiled base product (fused_gemm.hpp) with 4-bit weights or
+// the gate.
+#include "base_launch.hpp"
+#include "fused_gemm.hpp"
+
+namespace lora {
+namespace {
+
+template <WKind WK, bool GLU, bool G32>
+void launch(const FusedArgs& a, hipStream_t s) {
+  const dim3 grid(static_cast<unsigned>((a.n_tiles + 7) / 8 * 8));
+  if (a.ids) hipLaunchKernelGGL((k_fused_gemm<true, WK, GLU, G32>), grid, dim3(kFgThreads), 0, s, a);
+  else hipLaunchKernelGGL((k_fused_gemm<false, WK, GLU, G32>), grid, dim3(kFgThreads), 0, s, a);
+}
+
+template <WKind WK, bool GLU>
+void by_group(const FusedArgs& a, int32_t group, hipStream_t s) {
+  if (group == 32) launch<WK, GLU, true>(a, s);
+  else launch<WK, GLU, false>(a, s);
+}
+
+}  // namespace
+
+lora_status launch_tiles(const BaseCall& c, hipStream_t s) {
+  FusedArgs a{};
+  a.pv = c.pv;
+  a.x = c.x;
+  a.w[0] = c.w[0];
+  a.w[1] = c.w[1];
+  a.ids = c.ids;
+  a.y = c.y;
+  a.ld_x = c.ld_x;
+  a.ld_w = c.ld_w;
+  a.ld_y = c.ld_y;
+  a.n = c.n;
+  a.h_in = c.h_in;
+  a.h_out = c.h_out;
+  a.module[0] = c.module[0];
+  a.module[1] = c.module[1];
+  a.act = c.act;
+  a.group_shift = c.group == 128 ? 2 : c.group == 64 ? 1 : 0;
+  const int tc = c.glu ? kFgGluCols : kFgBN;
+  a.n_ct = (c.h_out + tc - 1) / tc;
+  const int64_t tiles = (static_cast<int64_t>(c.n) + kFgBM - 1) / kFgBM * a.n_ct;
+  if (tiles > (int64_t(1) << 22)) return LORA_ERR_SHAPE;   // 512 threads each: within a launch's 2^32 - 1
+  a.n_tiles = static_cast<int32_t>(tiles);
+  if (c.glu) {
+    switch (c.kind) {
+      case WKind::kBf16: launch<WKind::kBf16, true, false>(a, s); break;
+      case WKind::kFp8: launch<WKind::kFp8, true, false>(a, s); break;
+      case WKind::kInt4: by_group<WKind::kInt4, true>(a, c.group, s); break;
+      case WKind::kTable4: by_group<WKind::kTable4, true>(a, c.group, s); break;
+    }
+  } else if (c.kind == WKind::kInt4) {
+    by_group<WKind::kInt4, false>(a, c.group, s);
+  } else {
+    by_group<WKind::kTable4, false>(a, c.group, s);
+  }
+  return hipGetLastError() == hipSuccess ? LORA_OK : LORA_ERR_HIP;
+}
+
+}  // namespace lora
