@@ -714,14 +714,14 @@ lora_status fused_call(const lora_pool* p, int32_t module, const void* x, int64_
   hipStream_t s = static_cast<hipStream_t>(stream);
   if (w8) {
     if (ids)
-      hipLaunchKernelGGL((k_fused_gemm<true, WKind::kFp8>), dim3(grid), dim3(kFgThreads), 0, s, fa);
+      hipLaunchKernelGGL((k_fused_gemm<FgLora::kRide, WKind::kFp8>), dim3(grid), dim3(kFgThreads), 0, s, fa);
     else
-      hipLaunchKernelGGL((k_fused_gemm<false, WKind::kFp8>), dim3(grid), dim3(kFgThreads), 0, s, fa);
+      hipLaunchKernelGGL((k_fused_gemm<FgLora::kNone, WKind::kFp8>), dim3(grid), dim3(kFgThreads), 0, s, fa);
   } else {
     if (ids)
-      hipLaunchKernelGGL((k_fused_gemm<true, WKind::kBf16>), dim3(grid), dim3(kFgThreads), 0, s, fa);
+      hipLaunchKernelGGL((k_fused_gemm<FgLora::kRide, WKind::kBf16>), dim3(grid), dim3(kFgThreads), 0, s, fa);
     else
-      hipLaunchKernelGGL((k_fused_gemm<false, WKind::kBf16>), dim3(grid), dim3(kFgThreads), 0, s, fa);
+      hipLaunchKernelGGL((k_fused_gemm<FgLora::kNone, WKind::kBf16>), dim3(grid), dim3(kFgThreads), 0, s, fa);
   }
   return hipGetLastError() == hipSuccess ? LORA_OK : LORA_ERR_HIP;
 }

@@ -1,9 +1,10 @@
 // C ABI of the base products with 4-bit weights and of the gated feed-forward
 // product: argument checks and path selection.
+#include <algorithm>
+
 #include "base_launch.hpp"
 #include "fused_gemm.hpp"
 #include "pool.hpp"
-#include "rows_kernels.hpp"
 
 using namespace lora;
 
@@ -14,6 +15,12 @@ namespace {
 constexpr int32_t kRowsMaxTokens = 64;
 
 bool takes_rows(int32_t n_tokens) { return n_tokens <= kRowsMaxTokens; }
+
+// Workspace that a call with ids needs at least (a shorter one only limits the split of h_in).
+size_t ws_need(int n_proj, int32_t n_tokens, int64_t h_in, int64_t h_out) {
+  return takes_rows(n_tokens) ? rows_bytes(1, n_proj, n_tokens, h_out)
+                              : tiles_ws_bytes(n_proj, n_tokens, static_cast<int32_t>(h_in));
+}
 
 bool aligned(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
@@ -63,8 +70,7 @@ lora_status base_call(const lora_pool* p, BaseCall& c, const int32_t* module, co
   const int n_proj = c.glu ? 2 : 1;
   const int64_t h_out = p->h_out[module[0]];
   if (ws_bytes > 0 && (!ws || !aligned(ws, 16))) return LORA_ERR_ARG;
-  const bool rows = takes_rows(n_tokens);
-  if (rows && ids && ws_bytes < rows_ws_bytes(n_proj, n_tokens, h_out)) return LORA_ERR_WORKSPACE;
+  if (ids && ws_bytes < ws_need(n_proj, n_tokens, p->h_in[module[0]], h_out)) return LORA_ERR_WORKSPACE;
   if (n_tokens == 0) return LORA_OK;
   DeviceGuard g(p->device);
   if (!g.ok) return LORA_ERR_HIP;
@@ -80,8 +86,14 @@ lora_status base_call(const lora_pool* p, BaseCall& c, const int32_t* module, co
   c.module[0] = module[0];
   c.module[1] = module[n_proj - 1];
   c.ws = static_cast<float*>(ws);
+  c.ws_bytes = ws_bytes;
   hipStream_t s = static_cast<hipStream_t>(stream);
-  return rows ? launch_rows(c, s) : launch_tiles(c, s);
+  if (takes_rows(n_tokens)) return launch_rows(c, s);
+  if (ids) {
+    const lora_status st = launch_shrink(c, tiles_splits(c.n, c.h_in), s);
+    if (st != LORA_OK) return st;
+  }
+  return launch_tiles(c, s);
 }
 
 bool bad_act(lora_act act) { return act != LORA_ACT_SILU && act != LORA_ACT_GELU && act != LORA_ACT_GELU_TANH; }
@@ -92,7 +104,12 @@ extern "C" {
 
 size_t lora_fused_workspace_bytes(const lora_pool* p, int32_t module, int32_t n_proj, int32_t n_tokens) {
   if (!p || module < 0 || module >= p->n_modules || n_proj < 1 || n_proj > 2 || n_tokens < 1) return 0;
-  return takes_rows(n_tokens) ? rows_ws_bytes(n_proj, n_tokens, p->h_out[module]) : 0;
+  if (!takes_rows(n_tokens)) return tiles_ws_bytes(n_proj, n_tokens, static_cast<int32_t>(p->h_in[module]));
+  size_t most = 0;
+  for (WKind k : {WKind::kBf16, WKind::kFp8, WKind::kInt4})
+    most = std::max(most, rows_ws_bytes(k, n_proj, n_tokens, static_cast<int32_t>(p->h_in[module]),
+                                        static_cast<int32_t>(p->h_out[module])));
+  return most;
 }
 
 lora_status lora_fused_gemm_w4(const lora_pool* p, int32_t module, const void* x, int64_t ld_x, const lora_w4* w,

@@ -72,10 +72,16 @@ struct W4Table {
 
 // Eight codes of a word as the eight bf16 integers q (kInt4) or codebook
 // values (kTable4), in order of k.
-template <WKind WK>
+// EVEN_ODD (kInt4): in the order 0 2 4 6 1 3 5 7 instead, two instructions less.
+template <WKind WK, bool EVEN_ODD = false>
 __device__ __forceinline__ bf16x8 w4_widen(uint32_t w, const W4Table& tab) {
   uint32_t n[2];
-  w4_bytes(w, n);
+  if constexpr (EVEN_ODD && WK == WKind::kInt4) {
+    n[0] = w & 0x0F0F0F0Fu;
+    n[1] = (w >> 4) & 0x0F0F0F0Fu;
+  } else {
+    w4_bytes(w, n);
+  }
   if constexpr (WK == WKind::kTable4) {
     const u32x2 a = tab.look(n[0]), b = tab.look(n[1]);
     return __builtin_bit_cast(bf16x8, u32x4{a.x, a.y, b.x, b.y});
@@ -83,6 +89,12 @@ __device__ __forceinline__ bf16x8 w4_widen(uint32_t w, const W4Table& tab) {
     return __builtin_bit_cast(bf16x8, u32x4{w4_int2<false>(n[0]), w4_int2<true>(n[0]), w4_int2<false>(n[1]),
                                               w4_int2<true>(n[1])});
   }
+}
+
+// Eight bf16 values in the order that EVEN_ODD widening gives the codes.
+__device__ __forceinline__ u32x4 w4_xl_order(u32x4 v) {
+  return u32x4{__builtin_amdgcn_perm(v.y, v.x, 0x05040100u), __builtin_amdgcn_perm(v.w, v.z, 0x05040100u),
+               __builtin_amdgcn_perm(v.y, v.x, 0x07060302u), __builtin_amdgcn_perm(v.w, v.z, 0x07060302u)};
 }
 
 // Eight codes of a word as the eight bf16 integers q - z, exactly (|q - z| < 256).

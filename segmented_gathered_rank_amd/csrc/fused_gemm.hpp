@@ -32,6 +32,12 @@
 // significand bits) and multiplied by B on the same MFMA shape into the base
 // accumulators.  Rows an adapter does not have read the pool's zero page.
 //
+// Given t (FgLora::kGiven).  The callers that have a workspace compute t of
+// every token first (k_long_shrink: x is read once more, 2 bytes for every
+// 2 h_out flops), and the tile only expands: no rank rows ride along, so the
+// K loop is the plain product's, and a tile's further units cost an expand
+// instead of another pass over K.
+//
 // Gated pass (GLU): h = act(x Wg + term) * (x Wu + term).  A tile is 256 tokens
 // x 128 output columns of both projections: of a wave's four 16-column blocks
 // two are gate columns and two are the up columns of the same outputs, so the
@@ -80,10 +86,12 @@ struct FusedArgs {
   WView w[2];             // W^T of the projection, or of gate and up: row c = weights of output column c
   const int32_t* ids;     // [n]; unused by the base-only kernel
   __bf16* y;              // [n][ld_y], written
+  const float* t;         // given t: [split][projection][n][kMaxRank], scaled, zero past the rank in its last 16
   int64_t ld_x, ld_w, ld_y;   // ld_w in bytes
   int32_t n, h_in, h_out;
   int32_t module[2];
   int32_t act;            // gated pass: lora_act
+  int32_t t_splits;       // given t: to be added up
   int32_t group_shift;    // 4-bit: log2(group / 32)
   int32_t n_ct;           // column tiles
   int32_t n_tiles;        // row tiles x column tiles
@@ -176,12 +184,17 @@ __device__ __forceinline__ uint32_t fg_e4m3x2_to_bf16x2(uint32_t w, bool high) {
   return __builtin_bit_cast(uint32_t, v);
 }
 
-// LORA false: base product only.  WK: storage of W^T.  kFp8: e4m3 codes with a
+// Where a pass takes its adapters' t from: no adapters, the shrink riding along
+// with the base product, or computed before.
+enum class FgLora : int { kNone, kRide, kGiven };
+
+// WK: storage of W^T.  kFp8: e4m3 codes with a
 // scale per output column (W8A16: the codes are widened to bf16 on their way
 // into LDS, exactly, and the column scale multiplies the base product before
 // the adapter term is added).  G32: 4-bit groups of 32 (else 64 or more).
-template <bool LORA, WKind WK, bool GLU = false, bool G32 = false>
+template <FgLora L, WKind WK, bool GLU = false, bool G32 = false>
 __global__ __launch_bounds__(kFgThreads, 1) void k_fused_gemm(FusedArgs a) {
+  constexpr bool LORA = L != FgLora::kNone;
   constexpr bool W8 = WK == WKind::kFp8, W4 = is_w4(WK);
   constexpr int NP = fg_np(GLU);
   constexpr int TC = GLU ? kFgGluCols : kFgBN;   // output columns per tile
@@ -357,7 +370,7 @@ __global__ __launch_bounds__(kFgThreads, 1) void k_fused_gemm(FusedArgs a) {
   // B rows bpid[u][rank row][page - cp0] over the tile's columns; the zero
   // page stands in for rows past the rank
   auto load_pids = [&](int u0, int np) {
-    const int na = np * 16 * ppr_a;
+    const int na = L == FgLora::kRide ? np * 16 * ppr_a : 0;
     for (int i = tid; i < na; i += kFgThreads) {
       const int u = i / (16 * ppr_a), rest = i - u * 16 * ppr_a;
       const int jr = rest / ppr_a, kp = rest - jr * ppr_a;
@@ -425,8 +438,8 @@ __global__ __launch_bounds__(kFgThreads, 1) void k_fused_gemm(FusedArgs a) {
 
   // One K step of the base product from 4-bit codes: the step's sums start
   // from zero and join the accumulators times their group's scale.
-  auto step_w4 = [&](auto P_, int buf) {
-    constexpr int P = decltype(P_)::value;
+  static_assert(!W4 || L != FgLora::kRide, "4-bit steps carry no adapter units");
+  auto step_w4 = [&](int buf) {
     if constexpr (W4) {
       const unsigned char* Xs = sh.stage[buf][0];
       const unsigned char* Ws = sh.stage[buf][1];
@@ -443,7 +456,6 @@ __global__ __launch_bounds__(kFgThreads, 1) void k_fused_gemm(FusedArgs a) {
         }
       }
       const f32x4 none{0.f, 0.f, 0.f, 0.f};
-      bf16x8 xs[2][SB];
 #pragma unroll
       for (int tb = 0; tb < 8; ++tb) {
         bf16x8 xf[2];
@@ -462,24 +474,8 @@ __global__ __launch_bounds__(kFgThreads, 1) void k_fused_gemm(FusedArgs a) {
           sum[cb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf[1][cb], xf[1], G32 ? none : sum[cb], 0, 0, 0);
 #pragma unroll
         for (int cb = 0; cb < CB; ++cb) acc[cb][tb] += sc[G32 ? 1 : 0][cb] * sum[cb];
-        if constexpr (P > 0) {
-#pragma unroll
-          for (int ks = 0; ks < 2; ++ks) {
-            if (tb < SB) xs[ks][tb] = xf[ks];
-            else xs[ks][tb % SB] = tb / SB == wn ? xf[ks] : xs[ks][tb % SB];
-          }
-        }
-      }
-      if constexpr (P > 0) {
-#pragma unroll
-        for (int ks = 0; ks < 2; ++ks)
-#pragma unroll
-          for (int u = 0; u < P; ++u) {
-            const bf16x8 af = fg_lds8(sh.astage[buf], fg_swz(16 * u + l16, 4 * ks + lq));
-#pragma unroll
-            for (int i = 0; i < SB; ++i)
-              tacc[i][u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(af, xs[ks][i], tacc[i][u], 0, 0, 0);
-          }
+        // keeps the next blocks' reads from being hoisted: registers are the limit
+        __builtin_amdgcn_sched_barrier(0);
       }
     }
   };
@@ -498,7 +494,7 @@ __global__ __launch_bounds__(kFgThreads, 1) void k_fused_gemm(FusedArgs a) {
       const unsigned char* Xs = sh.stage[buf][0];
       const unsigned char* Ws = sh.stage[buf][1];
       if constexpr (BASE && W4) {
-        step_w4(P_, buf);
+        step_w4(buf);
         return;
       }
 #pragma unroll
@@ -557,10 +553,34 @@ __global__ __launch_bounds__(kFgThreads, 1) void k_fused_gemm(FusedArgs a) {
   // t of units u0 .. u0 + P - 1 -> LDS, masked to each unit's adapter and
   // rank rows and scaled; then acc^T += B^T_u [cols x 32] . T_u [32 x tokens]
   // where k 0..15 pair hi with ranks 0..15 and k 16..31 pair lo with them
+  auto multiply_b = [&](auto P_) {
+    constexpr int P = decltype(P_)::value;
+    const unsigned char* T_s = idle;                           // [256 tokens][kFgTRow]
+    const unsigned char* B_s = idle + kFgTileBytes + kFgBOff;  // [u][16 ranks][256 cols] bf16
+#pragma unroll
+    for (int u = 0; u < P; ++u) {
+      bf16x8 bfr[CB];   // lane: output column wrow + 16 cb, ranks 8 (lq & 1) .. +8
+#pragma unroll
+      for (int cb = 0; cb < CB; ++cb) {
+        const unsigned short* bp = reinterpret_cast<const unsigned short*>(
+            B_s + u * 8192 + (8 * (lq & 1)) * 512 + 2 * (wrow + 16 * cb));
+        unsigned short e[8];
+#pragma unroll
+        for (int r = 0; r < 8; ++r) e[r] = bp[256 * r];
+        bfr[cb] = __builtin_bit_cast(bf16x8, e);
+      }
+#pragma unroll
+      for (int tb = 0; tb < 8; ++tb) {
+        const bf16x8 tf = fg_lds8(T_s, (xrow + 16 * tb) * kFgTRow + u * 64 + 16 * lq);
+#pragma unroll
+        for (int cb = 0; cb < CB; ++cb)
+          acc[cb][tb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bfr[cb], tf, acc[cb][tb], 0, 0, 0);
+      }
+    }
+  };
   auto expand = [&](auto P_, int u0) {
     constexpr int P = decltype(P_)::value;
-    unsigned char* T_s = idle;                                 // [256 tokens][kFgTRow]
-    const unsigned char* B_s = idle + kFgTileBytes + kFgBOff;  // [u][16 ranks][256 cols] bf16
+    unsigned char* T_s = idle;
 #pragma unroll
     for (int i = 0; i < SB; ++i) {
       const int tok = srow + 16 * i;
@@ -588,26 +608,7 @@ __global__ __launch_bounds__(kFgThreads, 1) void k_fused_gemm(FusedArgs a) {
       }
     }
     __syncthreads();
-#pragma unroll
-    for (int u = 0; u < P; ++u) {
-      bf16x8 bfr[CB];   // lane: output column wrow + 16 cb, ranks 8 (lq & 1) .. +8
-#pragma unroll
-      for (int cb = 0; cb < CB; ++cb) {
-        const unsigned short* bp = reinterpret_cast<const unsigned short*>(
-            B_s + u * 8192 + (8 * (lq & 1)) * 512 + 2 * (wrow + 16 * cb));
-        unsigned short e[8];
-#pragma unroll
-        for (int r = 0; r < 8; ++r) e[r] = bp[256 * r];
-        bfr[cb] = __builtin_bit_cast(bf16x8, e);
-      }
-#pragma unroll
-      for (int tb = 0; tb < 8; ++tb) {
-        const bf16x8 tf = fg_lds8(T_s, (xrow + 16 * tb) * kFgTRow + u * 64 + 16 * lq);
-#pragma unroll
-        for (int cb = 0; cb < CB; ++cb)
-          acc[cb][tb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bfr[cb], tf, acc[cb][tb], 0, 0, 0);
-      }
-    }
+    multiply_b(P_);
   };
 
   // Output column of this lane's accumulators of block cb: + 0 .. 3.
@@ -627,8 +628,57 @@ __global__ __launch_bounds__(kFgThreads, 1) void k_fused_gemm(FusedArgs a) {
     }
   };
 
+  // ---- given t: the tile's units in pairs, t -> LDS as hi and lo parts
+  auto expand_given = [&](int u0) {
+    unsigned char* T_s = idle;
+    const int np = min(n_units - u0, kFgPassUnits);
+    load_pids(u0, np);
+    __syncthreads();   // also: the previous pair's reads (or the K loop's) are done
+    if (np == 2) load_b(fg_int<2>{}, u0, idle + kFgTileBytes + kFgBOff);
+    else load_b(fg_int<1>{}, u0, idle + kFgTileBytes + kFgBOff);
+    const int tok = tid >> 1, u = tid & 1;
+    f32x4 t[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) t[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    if (u < np) {
+      const int un = sh.unit[u0 + u];
+      if (sh.dslot[un >> 3] == sh.ids[tok]) {   // rows past the batch have id -1: no slot
+        const float* from =
+            a.t + (static_cast<int64_t>((un >> 2) & (NP - 1)) * a.n + row0 + tok) * kMaxRank + 16 * (un & 3);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) t[i] = reinterpret_cast<const f32x4*>(from)[i];
+        for (int z = 1; z < a.t_splits; ++z) {
+          from += static_cast<int64_t>(NP) * a.n * kMaxRank;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) t[i] += reinterpret_cast<const f32x4*>(from)[i];
+        }
+      }
+    }
+    __bf16 hi[16], lo[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      hi[i] = static_cast<__bf16>(t[i >> 2][i & 3]);
+      lo[i] = static_cast<__bf16>(t[i >> 2][i & 3] - static_cast<float>(hi[i]));
+    }
+    unsigned char* trow = T_s + tok * kFgTRow + u * 64;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      *reinterpret_cast<bf16x8*>(trow + 16 * i) = *reinterpret_cast<const bf16x8*>(hi + 8 * i);
+      *reinterpret_cast<bf16x8*>(trow + 32 + 16 * i) = *reinterpret_cast<const bf16x8*>(lo + 8 * i);
+    }
+    __syncthreads();
+    if (np == 2) multiply_b(fg_int<2>{});
+    else multiply_b(fg_int<1>{});
+    __syncthreads();
+  };
+
   // ---- pass 0: the base product with up to two units
-  if constexpr (LORA) {
+  if constexpr (L == FgLora::kGiven) {
+    __syncthreads();   // stage 0 has landed
+    kloop(fg_int<0>{}, fg_int<1>{}, 0);
+    scale_base();
+    for (int u0 = 0; u0 < n_units; u0 += kFgPassUnits) expand_given(u0);
+  } else if constexpr (LORA) {
     const int np0 = min(n_units, kFgPassUnits);
     if (np0 > 0) {
       load_pids(0, np0);

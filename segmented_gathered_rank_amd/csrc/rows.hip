@@ -1,37 +1,63 @@
 // Launches of the row-streaming base product (rows_kernels.hpp).
+#include <algorithm>
+
 #include "base_launch.hpp"
 #include "rows_kernels.hpp"
 
 namespace lora {
 namespace {
 
-template <WKind WK, int G, int TB, bool GLU>
-void launch(const RowsArgs& base, hipStream_t s) {
-  constexpr int CB = GLU ? 2 : 1;
-  RowsArgs a = base;
-  a.n_blocks = a.h_out / (16 * (GLU ? CB / 2 : CB));
-  const unsigned gx = static_cast<unsigned>(a.n_units + (a.n_blocks + 7) / 8 * 8);
-  const unsigned gy = static_cast<unsigned>((a.n + kRowsTokens - 1) / kRowsTokens);
-  hipLaunchKernelGGL((k_rows<WK, G, TB, CB, GLU>), dim3(gx, gy), dim3(kRowsThreads), 0, s, a);
+constexpr int kRowsCB = 2;   // 16-row blocks of W^T to a wave
+
+struct RowsPlan {
+  int tb;        // 16-token blocks of a workgroup: 1, 2 or 4
+  bool x_lds;    // k_rows, else k_mid
+  int blocks;    // base workgroups of one split and chunk
+  int chunks;    // of 16 * tb tokens
+  int splits;    // of h_in over workgroups
+};
+
+// Base workgroups that a split of h_in aims at.
+constexpr int kRowsWgTarget = 256;
+
+RowsPlan rows_plan(WKind kind, int n_proj, int32_t n, int32_t h_in, int32_t h_out, size_t ws_bytes) {
+  RowsPlan p{};
+  p.tb = n <= 16 ? 1 : n <= 32 ? 2 : 4;
+  p.chunks = (n + 16 * p.tb - 1) / (16 * p.tb);
+  auto split = [&](int cols, int steps, int min_steps) {
+    p.blocks = (h_out * n_proj + cols - 1) / cols;
+    p.splits = std::max(1, std::min({kRowsMaxSplits, kRowsWgTarget / (p.blocks * p.chunks), steps / min_steps}));
+    while (p.splits > 1 && rows_bytes(p.splits, n_proj, n, h_out) > ws_bytes) --p.splits;
+  };
+  const int ks = is_w4(kind) ? 128 : kind == WKind::kFp8 ? 64 : 32, steps = (h_in + ks - 1) / ks;
+  if (p.tb == 1) {
+    split(16 * kRowsCB, steps, kRowsWaves);
+    const int range = ((steps + p.splits - 1) / p.splits + 1) * ks;   // at most, of one workgroup
+    p.x_lds = n * rows_x_stride(range) <= kRowsXBytes;
+  }
+  if (!p.x_lds) split(16 * kRowsCB * kRowsWaves, (h_in + 127) / 128, 2);
+  return p;
 }
 
 template <WKind WK, int G, bool GLU>
-void by_tokens(const RowsArgs& a, hipStream_t s) {
-  if (a.n <= 16) launch<WK, G, 1, GLU>(a, s);
-  else if (a.n <= 32) launch<WK, G, 2, GLU>(a, s);
-  else launch<WK, G, 4, GLU>(a, s);
+void by_tokens(const RowsArgs& base, const RowsPlan& p, hipStream_t s) {
+  RowsArgs a = base;
+  a.n_blocks = p.blocks;
+  const dim3 grid(static_cast<unsigned>(a.n_units + (a.n_blocks + 7) / 8 * 8), p.chunks, p.splits), wg(kRowsThreads);
+  if (p.x_lds) hipLaunchKernelGGL((k_rows<WK, G, kRowsCB, GLU>), grid, wg, 0, s, a);
+  else if (p.tb == 1) hipLaunchKernelGGL((k_mid<WK, G, 1, kRowsCB, GLU>), grid, wg, 0, s, a);
+  else if (p.tb == 2) hipLaunchKernelGGL((k_mid<WK, G, 2, kRowsCB, GLU>), grid, wg, 0, s, a);
+  else hipLaunchKernelGGL((k_mid<WK, G, 4, kRowsCB, GLU>), grid, wg, 0, s, a);
 }
 
 template <WKind WK, bool GLU>
-void by_group(const RowsArgs& a, int32_t group, hipStream_t s) {
-  if (group == 32) by_tokens<WK, 32, GLU>(a, s);
-  else if (group == 64) by_tokens<WK, 64, GLU>(a, s);
-  else by_tokens<WK, 128, GLU>(a, s);
+void by_group(const RowsArgs& a, const RowsPlan& p, int32_t group, hipStream_t s) {
+  if (group == 32) by_tokens<WK, 32, GLU>(a, p, s);
+  else if (group == 64) by_tokens<WK, 64, GLU>(a, p, s);
+  else by_tokens<WK, 128, GLU>(a, p, s);
 }
 
-}  // namespace
-
-lora_status launch_rows(const BaseCall& c, hipStream_t s) {
+RowsArgs rows_args(const BaseCall& c) {
   RowsArgs a{};
   a.pv = c.pv;
   a.w[0] = c.w[0];
@@ -48,27 +74,48 @@ lora_status launch_rows(const BaseCall& c, hipStream_t s) {
   a.module[0] = c.module[0];
   a.module[1] = c.module[1];
   a.act = c.act;
+  return a;
+}
+
+}  // namespace
+
+size_t rows_ws_bytes(WKind kind, int n_proj, int32_t n, int32_t h_in, int32_t h_out) {
+  return rows_bytes(rows_plan(kind, n_proj, n, h_in, h_out, SIZE_MAX).splits, n_proj, n, h_out);
+}
+
+lora_status launch_shrink(const BaseCall& c, int splits, hipStream_t s) {
+  RowsArgs a = rows_args(c);
+  a.t = c.ws;
+  const dim3 grid((c.n + kRowsTokens - 1) / kRowsTokens, splits);
+  hipLaunchKernelGGL(k_long_shrink, grid, dim3(kRowsThreads), 0, s, a, c.glu ? 2 : 1);
+  return hipGetLastError() == hipSuccess ? LORA_OK : LORA_ERR_HIP;
+}
+
+lora_status launch_rows(const BaseCall& c, hipStream_t s) {
+  RowsArgs a = rows_args(c);
   const int n_proj = c.glu ? 2 : 1;
+  const RowsPlan p = rows_plan(c.kind, n_proj, c.n, c.h_in, c.h_out, c.ws_bytes);
+  a.splits = p.splits;
+  if (c.ids || p.splits > 1) a.part = c.ws;
   if (c.ids) {
-    a.part = c.ws;
-    a.t = c.ws + static_cast<int64_t>(n_proj) * c.n * c.h_out;
-    const int units = (c.n < kRowsTokens ? c.n : kRowsTokens) * n_proj * ((c.pv.max_rank + 15) / 16);
+    a.t = c.ws + static_cast<int64_t>(p.splits) * n_proj * c.n * c.h_out;
+    const int units = std::min(c.n, 16 * p.tb) * n_proj * ((c.pv.max_rank + 15) / 16);
     a.n_units = (units + 7) / 8 * 8;
   }
   if (c.glu) {
     switch (c.kind) {
-      case WKind::kBf16: by_tokens<WKind::kBf16, 0, true>(a, s); break;
-      case WKind::kFp8: by_tokens<WKind::kFp8, 0, true>(a, s); break;
-      case WKind::kInt4: by_group<WKind::kInt4, true>(a, c.group, s); break;
-      case WKind::kTable4: by_group<WKind::kTable4, true>(a, c.group, s); break;
+      case WKind::kBf16: by_tokens<WKind::kBf16, 0, true>(a, p, s); break;
+      case WKind::kFp8: by_tokens<WKind::kFp8, 0, true>(a, p, s); break;
+      case WKind::kInt4: by_group<WKind::kInt4, true>(a, p, c.group, s); break;
+      case WKind::kTable4: by_group<WKind::kTable4, true>(a, p, c.group, s); break;
     }
   } else if (c.kind == WKind::kInt4) {
-    by_group<WKind::kInt4, false>(a, c.group, s);
+    by_group<WKind::kInt4, false>(a, p, c.group, s);
   } else {
-    by_group<WKind::kTable4, false>(a, c.group, s);
+    by_group<WKind::kTable4, false>(a, p, c.group, s);
   }
   if (hipGetLastError() != hipSuccess) return LORA_ERR_HIP;
-  if (c.ids) {
+  if (a.part) {
     const dim3 grid((c.h_out / 4 + kFinishThreads - 1) / kFinishThreads, c.n);
     if (c.glu) hipLaunchKernelGGL((k_rows_finish<true>), grid, dim3(kFinishThreads), 0, s, a);
     else hipLaunchKernelGGL((k_rows_finish<false>), grid, dim3(kFinishThreads), 0, s, a);

@@ -22,9 +22,7 @@
 //
 // Adapters.  t = s_a x A_a^T is the same kind of product with A's rank rows
 // as the weights; its workgroups come first in the grid, one for each
-// 16-row block of each token's adapter (the first token of an adapter does
-// the work for all of the batch's tokens that share it; the others' leave at
-// once).  Base sums and t then go through the workspace to a second, small
+// 16-row block of each distinct adapter of a chunk's tokens.  Base sums and t then go through the workspace to a second, small
 // kernel that adds t B, applies the gate and rounds once.
 #pragma once
 
@@ -38,20 +36,27 @@ constexpr int kRowsTokens = 64;    // tokens of one workgroup; longer batches ru
 constexpr int kRowsMaxPpr = 32;    // A pages per rank row
 constexpr int kRowsTRow = kMaxRank;
 
+constexpr int kRowsXBytes = 64 * 1024;   // x in LDS: two workgroups to a CU
+
+// Bytes from token to token of x in LDS: 16 more than the row, so that the
+// tokens of one k start in different banks.
+__host__ __device__ constexpr int rows_x_stride(int k) { return 2 * k + 16; }
+
 struct RowsArgs {
   PoolView pv;
   WView w[2];             // one projection, or gate and up
   const __bf16* x;        // [n][ld_x]
   const int32_t* ids;     // [n] or null
   __bf16* y;              // [n][ld_y], written
-  float* part;            // [projection][n][h_out] base sums, with adapters
+  float* part;            // [split][projection][n][h_out] base sums, with adapters or several splits
   float* t;               // [projection][n][kRowsTRow] scaled shrink results, with adapters
   int64_t ld_x, ld_w, ld_y;   // ld_w in bytes
   int32_t n, h_in, h_out;
   int32_t module[2];
   int32_t act;
   int32_t n_units;        // shrink workgroups ahead of the base's (a multiple of 8)
-  int32_t n_blocks;       // base workgroups
+  int32_t n_blocks;       // base workgroups of one split
+  int32_t splits;         // of h_in, over workgroups (gridDim.z)
 };
 
 template <WKind WK> struct RowsLoad;   // one 16-byte load of a row, as MFMA A operands
@@ -74,101 +79,321 @@ __device__ __forceinline__ u32x4 rows_transpose4(u32x4 v) {
                static_cast<uint32_t>(d[1])};
 }
 
+// The d-th distinct adapter (in order of first use) of a chunk whose lanes hold
+// the tokens' ids: its id and the lanes that have it, or false.
+__device__ __forceinline__ bool rows_distinct(int mine, bool valid, int d, int* id, uint64_t* same) {
+  uint64_t left = __ballot(valid);
+  for (; left != 0; --d) {
+    *id = __builtin_amdgcn_readlane(mine, __builtin_ctzll(left));
+    *same = __ballot(valid && mine == *id);
+    if (d == 0) return true;
+    left &= ~*same;
+  }
+  return false;
+}
+
+template <int T>   // 16-token blocks a pass over K takes at most
 struct RowsShrinkShared {
   int32_t pid[16][kRowsMaxPpr];
   int32_t tok[kRowsTokens];
-  f32x4 red[kRowsWaves][64];
+  f32x4 red[kRowsWaves][T][64];
 };
 
-// t of one 16-row block of the adapter of token `tok0 + i`, for every token of
-// the chunk with that adapter.  Whole workgroup; returns early where another
-// unit does the work.
-__device__ __forceinline__ void rows_shrink(const RowsArgs& a, RowsShrinkShared& sh, int unit, int n_proj, int tok0,
-                                            int m) {
+// t of one 16-row block of adapter e for the n_tok tokens listed in sh.tok.
+template <int T, int TM>
+__device__ __forceinline__ void rows_shrink_block(const RowsArgs& a, RowsShrinkShared<TM>& sh, const SlotEntry& e,
+                                                  int p, int rb, int tok0, int n_tok, int lane, int wave) {
+  constexpr int U = T == 1 ? 8 : 4;
+  const int l16 = lane & 15, lq = lane >> 4;
+  const int h = static_cast<int>(a.pv.page_elems);
+  const __bf16* pages = static_cast<const __bf16*>(a.pv.pages);
+  const int n32 = a.h_in >> 5;
+  const int s0 = n32 * wave / kRowsWaves, s1 = n32 * (wave + 1) / kRowsWaves;
+  int tok[T];
+  const __bf16* xr[T];
+  f32x4 acc[T];
+#pragma unroll
+  for (int tb = 0; tb < T; ++tb) {
+    tok[tb] = sh.tok[min(16 * tb + l16, n_tok - 1)];
+    xr[tb] = a.x + static_cast<int64_t>(tok0 + tok[tb]) * a.ld_x + 8 * lq;
+    acc[tb] = f32x4{0.f, 0.f, 0.f, 0.f};
+  }
+  int kp = 32 * s0 / h, off = 32 * s0 - kp * h;
+  for (int s = s0; s < s1; s += U) {
+    u32x4 af[U];
+    bf16x8 xf[U][T];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      // past the wave's end the last step is read again and A counts as zero: a
+      // branch around the products would pull the loads into it, one by one
+      const int su = min(s + u, s1 - 1);
+      af[u] = *reinterpret_cast<const u32x4*>(pages + static_cast<int64_t>(sh.pid[l16][kp]) * h + off + 8 * lq);
+#pragma unroll
+      for (int tb = 0; tb < T; ++tb) xf[u][tb] = *reinterpret_cast<const bf16x8*>(xr[tb] + 32 * su);
+      if (su + 1 < s1) {
+        off += 32;
+        if (off == h) { off = 0; ++kp; }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const uint32_t live = s + u < s1 ? ~0u : 0u;
+      const bf16x8 av = __builtin_bit_cast(bf16x8, af[u] & u32x4{live, live, live, live});
+#pragma unroll
+      for (int tb = 0; tb < T; ++tb) acc[tb] = rows_mfma(av, xf[u][tb], acc[tb]);
+    }
+  }
+#pragma unroll
+  for (int tb = 0; tb < T; ++tb) sh.red[wave][tb][lane] = acc[tb];
+  __syncthreads();
+#pragma unroll
+  for (int tb = 0; tb < T; ++tb) {
+    if (wave != tb || 16 * tb + l16 >= n_tok) continue;
+    f32x4 v = sh.red[0][tb][lane];
+#pragma unroll
+    for (int w = 1; w < kRowsWaves; ++w) v += sh.red[w][tb][lane];
+    float* to = a.t + (static_cast<int64_t>(p) * a.n + tok0 + tok[tb]) * kRowsTRow + 16 * rb + 4 * lq;
+    *reinterpret_cast<f32x4*>(to) = v * e.scale;
+  }
+}
+
+// Shrink unit `unit` of the chunk of tokens tok0 .. tok0 + m - 1: (distinct
+// adapter, projection, 16-row block).  Whole workgroup; false when the chunk
+// has no such adapter (nor any later one).
+template <int TM>
+__device__ __forceinline__ bool rows_shrink(const RowsArgs& a, RowsShrinkShared<TM>& sh, int unit, int n_proj,
+                                            int tok0, int m) {
   // uniform: the matrix instructions ignore the execution mask, so what they
   // depend on must be a branch of the whole wave
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int rbs = (a.pv.max_rank + 15) >> 4;
-  const int i = unit / (n_proj * rbs), rest = unit - i * (n_proj * rbs);
+  const int d = unit / (n_proj * rbs), rest = unit - d * (n_proj * rbs);
   const int p = rest / rbs, rb = rest - p * rbs;
-  if (i >= m) return;
   const int mine = lane < m ? a.ids[tok0 + lane] : -1;
-  const int id = __builtin_amdgcn_readlane(mine, i);
-  if (id < 0 || id >= a.pv.n_slots) return;
-  const uint64_t same = __ballot(mine == id);
-  if ((same & ((uint64_t(1) << i) - 1)) != 0) return;   // an earlier token's unit does it
+  int id;
+  uint64_t same;
+  if (!rows_distinct(mine, mine >= 0 && mine < a.pv.n_slots, d, &id, &same)) return false;
   const SlotEntry e = a.pv.entries[static_cast<int64_t>(id) * a.pv.n_modules + a.module[p]];
-  if (e.rank <= 16 * rb) return;
+  if (e.rank <= 16 * rb) return true;
   const int n_tok = __popcll(same);
-  if (wave == 0 && mine == id) sh.tok[__popcll(same & ((uint64_t(1) << lane) - 1))] = lane;
-  const int h = static_cast<int>(a.pv.page_elems), ppr = a.h_in / h;
+  if (wave == 0 && (same >> lane & 1)) sh.tok[__popcll(same & ((uint64_t(1) << lane) - 1))] = lane;
+  const int ppr = a.h_in / static_cast<int>(a.pv.page_elems);
   for (int q = threadIdx.x; q < 16 * ppr; q += kRowsThreads) {
     const int r = q / ppr, kp = q - r * ppr, j = 16 * rb + r;
     sh.pid[r][kp] = j < e.rank ? a.pv.page_ids[e.a_off + j * ppr + kp] : a.pv.zero_page;
   }
   __syncthreads();
+  if (TM == 1 || n_tok <= 16) rows_shrink_block<1, TM>(a, sh, e, p, rb, tok0, n_tok, lane, wave);
+  else rows_shrink_block<TM, TM>(a, sh, e, p, rb, tok0, n_tok, lane, wave);
+  return true;
+}
+
+// t of every token of a long batch, for the tiled kernels.  A workgroup takes 64
+// tokens and one split of h_in: x goes through LDS 256 k at a time (read once
+// for up to kLsUnits units of 16 rank rows, in whole 256-byte runs: the 16-row
+// fragments of x, 64 bytes a row at a power-of-two stride, read straight from
+// memory took four times as long), wave w multiplies k 32 w .. + 32 of it by
+// every unit's rows for all 64 tokens, and each unit's tokens are picked when
+// t is written: [split][projection][n][kRowsTRow].
+constexpr int kLsUnits = 4;
+constexpr int kLsK = 256;
+
+__global__ __launch_bounds__(kRowsThreads) void k_long_shrink(RowsArgs a, int n_proj) {
+  struct Shared {
+    union {
+      alignas(16) unsigned char x[2][kRowsTokens * kLsK * 2];
+      f32x4 red[kRowsWaves][4][64];
+    };
+    int32_t pid[kLsUnits][16][kRowsMaxPpr];
+    int32_t unit_of[kLsUnits];     // id, projection and rank block of the pass's units
+    int32_t unit_p[kLsUnits], unit_rb[kLsUnits];
+  };
+  __shared__ Shared sh;
+  const int tok0 = blockIdx.x * kRowsTokens, m = min(a.n - tok0, kRowsTokens);
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int l16 = lane & 15, lq = lane >> 4;
+  const int h = static_cast<int>(a.pv.page_elems), ppr = a.h_in / h;
   const __bf16* pages = static_cast<const __bf16*>(a.pv.pages);
-  const int n32 = a.h_in >> 5;
-  const int s0 = n32 * wave / kRowsWaves, s1 = n32 * (wave + 1) / kRowsWaves;
-  for (int tb = 0; 16 * tb < n_tok; ++tb) {
-    const int tok = sh.tok[min(16 * tb + l16, n_tok - 1)];
-    const __bf16* xr = a.x + static_cast<int64_t>(tok0 + tok) * a.ld_x + 8 * lq;
-    f32x4 acc{0.f, 0.f, 0.f, 0.f};
-    int kp = 32 * s0 / h, off = 32 * s0 - kp * h;
-    constexpr int U = 8;
-    for (int s = s0; s < s1; s += U) {
-      bf16x8 af[U], xf[U];
+  const int steps = (a.h_in + kLsK - 1) / kLsK;
+  const int s0 = steps * blockIdx.y / gridDim.y, s1 = steps * (blockIdx.y + 1) / gridDim.y;
+  const int mine = lane < m ? a.ids[tok0 + lane] : -1;
+  const bool valid = mine >= 0 && mine < a.pv.n_slots;
+  uint64_t left = __ballot(valid);   // lanes whose adapters are still to come
+
+  // x: thread moves pieces of 16 bytes, 32 threads to a token's 512 bytes
+  const int xc = tid & 31;
+  const __bf16* xsrc[4];
+  int xdst[4];
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        // past the wave's end the last step is read again and not used
-        const int su = min(s + u, s1 - 1);
-        const __bf16* ap = pages + static_cast<int64_t>(sh.pid[l16][kp]) * h + off + 8 * lq;
-        af[u] = *reinterpret_cast<const bf16x8*>(ap);
-        xf[u] = *reinterpret_cast<const bf16x8*>(xr + 32 * su);
-        if (su + 1 < s1) {
-          off += 32;
-          if (off == h) { off = 0; ++kp; }
+  for (int q = 0; q < 4; ++q) {
+    const int r = (tid >> 5) + 16 * q;
+    xsrc[q] = a.x + static_cast<int64_t>(tok0 + min(r, m - 1)) * a.ld_x;
+    xdst[q] = r * (2 * kLsK) + ((xc ^ (r & 15)) << 4);
+  }
+  u32x4 xr[4];
+  auto load_x = [&](int s) {
+    const int k = s * kLsK + 8 * xc;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) xr[q] = *reinterpret_cast<const u32x4*>(xsrc[q] + (k < a.h_in ? k : 0));
+  };
+  auto store_x = [&](int s, int buf) {
+    const bool in = s * kLsK + 8 * xc < a.h_in;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      if (!in) xr[q] = u32x4{0u, 0u, 0u, 0u};
+      *reinterpret_cast<u32x4*>(sh.x[buf] + xdst[q]) = xr[q];
+    }
+  };
+
+  int p = 0, rb = 0;   // where the listing of units stands within the first adapter left
+  for (;;) {
+    // ---- the pass's units
+    int n_units = 0;
+    __syncthreads();   // the previous pass's reads are done
+    while (left != 0 && n_units < kLsUnits) {
+      const int id = __builtin_amdgcn_readlane(mine, __builtin_ctzll(left));
+      const int rank = a.pv.entries[static_cast<int64_t>(id) * a.pv.n_modules + a.module[p]].rank;
+      if (16 * rb < rank) {
+        if (tid == 0) {
+          sh.unit_of[n_units] = id;
+          sh.unit_p[n_units] = p;
+          sh.unit_rb[n_units] = rb;
+        }
+        ++n_units;
+        ++rb;
+      } else {
+        rb = 0;
+        if (++p == n_proj) {
+          p = 0;
+          left &= ~__ballot(valid && mine == id);
         }
       }
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (s + u < s1) acc = rows_mfma(af[u], xf[u], acc);
     }
-    sh.red[wave][lane] = acc;
+    if (n_units == 0) return;
+    if (s0 < s1) load_x(s0);
     __syncthreads();
-    if (wave == 0) {
-      f32x4 v = sh.red[0][lane];
+    for (int q = tid; q < n_units * 16 * ppr; q += kRowsThreads) {
+      const int u = q / (16 * ppr), rest = q - u * 16 * ppr, r = rest / ppr, kp = rest - r * ppr;
+      const SlotEntry e = a.pv.entries[static_cast<int64_t>(sh.unit_of[u]) * a.pv.n_modules + a.module[sh.unit_p[u]]];
+      const int j = 16 * sh.unit_rb[u] + r;
+      sh.pid[u][r][kp] = j < e.rank ? a.pv.page_ids[e.a_off + j * ppr + kp] : a.pv.zero_page;
+    }
+    if (s0 < s1) store_x(s0, 0);
+    __syncthreads();
+
+    // ---- the wave's k of the split
+    f32x4 acc[kLsUnits][4];
 #pragma unroll
-      for (int w = 1; w < kRowsWaves; ++w) v += sh.red[w][lane];
-      if (16 * tb + l16 < n_tok) {
-        float* to = a.t + (static_cast<int64_t>(p) * a.n + tok0 + tok) * kRowsTRow + 16 * rb + 4 * lq;
-        *reinterpret_cast<f32x4*>(to) = v * e.scale;
+    for (int u = 0; u < kLsUnits; ++u)
+#pragma unroll
+      for (int tb = 0; tb < 4; ++tb) acc[u][tb] = f32x4{0.f, 0.f, 0.f, 0.f};
+    bf16x8 af[kLsUnits];
+    auto load_a = [&](int s) {
+      const int k = min(s * kLsK + 32 * wave, a.h_in - 32);   // past the end x is zero
+      const int kp = k / h, off = k - kp * h + 8 * lq;
+#pragma unroll
+      for (int u = 0; u < kLsUnits; ++u)
+        af[u] = *reinterpret_cast<const bf16x8*>(
+            pages + static_cast<int64_t>(sh.pid[min(u, n_units - 1)][l16][kp]) * h + off);
+    };
+    if (s0 < s1) load_a(s0);
+    for (int s = s0; s < s1; ++s) {
+      const int buf = (s - s0) & 1;
+      bf16x8 av[kLsUnits];
+#pragma unroll
+      for (int u = 0; u < kLsUnits; ++u) av[u] = af[u];
+      if (s + 1 < s1) {
+        load_x(s + 1);
+        load_a(s + 1);
       }
+#pragma unroll
+      for (int tb = 0; tb < 4; ++tb) {
+        const bf16x8 xf = *reinterpret_cast<const bf16x8*>(sh.x[buf] + (16 * tb + l16) * (2 * kLsK) +
+                                                           (((4 * wave + lq) ^ l16) << 4));
+#pragma unroll
+        for (int u = 0; u < kLsUnits; ++u) acc[u][tb] = rows_mfma(av[u], xf, acc[u][tb]);
+      }
+      if (s + 1 < s1) store_x(s + 1, buf ^ 1);
+      __syncthreads();
     }
-    __syncthreads();
+
+    // ---- the waves' sums of each unit, in wave order
+    for (int u = 0; u < n_units; ++u) {
+#pragma unroll
+      for (int v = 0; v < kLsUnits; ++v)
+        if (u == v) {
+#pragma unroll
+          for (int tb = 0; tb < 4; ++tb) sh.red[wave][tb][lane] = acc[v][tb];
+        }
+      __syncthreads();
+      if (wave < 4) {
+        f32x4 v = sh.red[0][wave][lane];
+#pragma unroll
+        for (int w = 1; w < kRowsWaves; ++w) v += sh.red[w][wave][lane];
+        const int tok = 16 * wave + l16, id = sh.unit_of[u], up = sh.unit_p[u];
+        if (tok < m && a.ids[tok0 + tok] == id) {
+          const float scale = a.pv.entries[static_cast<int64_t>(id) * a.pv.n_modules + a.module[up]].scale;
+          const int64_t row = (static_cast<int64_t>(blockIdx.y) * n_proj + up) * a.n + tok0 + tok;
+          *reinterpret_cast<f32x4*>(a.t + row * kRowsTRow + 16 * sh.unit_rb[u] + 4 * lq) = v * scale;
+        }
+      }
+      __syncthreads();
+    }
   }
 }
 
-// WK: storage of W.  G: k of one 4-bit group (else 0).  TB: 16-token blocks.
-// CB: 16-row blocks of W^T a workgroup takes; with GLU half of them gate
-// rows and half up rows of the same output columns.
-template <WKind WK, int G, int TB, int CB, bool GLU>
+// Four columns of a token's base sums of one projection, to the workspace.
+__device__ __forceinline__ void rows_put_part(const RowsArgs& a, int n_proj, int p, int tok, int c, f32x4 v) {
+  const int64_t row = static_cast<int64_t>(blockIdx.z * n_proj + p) * a.n + tok;
+  *reinterpret_cast<f32x4*>(a.part + row * a.h_out + c) = v;
+}
+
+// Four columns of a token's output: v, or act(v) * up.
+template <bool GLU>
+__device__ __forceinline__ void rows_put(const RowsArgs& a, int tok, int c, f32x4 v, f32x4 up) {
+  __bf16 o[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) o[e] = static_cast<__bf16>(GLU ? glu_act(a.act, v[e]) * up[e] : v[e]);
+  *reinterpret_cast<u32x2*>(a.y + static_cast<int64_t>(tok) * a.ld_y + c) = __builtin_bit_cast(u32x2, o);
+}
+
+// Sixteen e4m3 codes' half h (8 codes) widened to bf16, exactly.
+__device__ __forceinline__ bf16x8 rows_fp8(u32x4 v, int h) {
+  u32x4 o;
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const bf16x2 lo = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v[2 * h + j], 1.0f, false);
+    const bf16x2 hi = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v[2 * h + j], 1.0f, true);
+    o[2 * j] = __builtin_bit_cast(uint32_t, lo);
+    o[2 * j + 1] = __builtin_bit_cast(uint32_t, hi);
+  }
+  return __builtin_bit_cast(bf16x8, o);
+}
+
+// Up to 16 tokens whose x fits in LDS.  WK: storage of W.  G: k of one 4-bit
+// group (else 0).  CB: 16-row blocks of W^T a workgroup takes; with GLU half of
+// them gate rows and half up rows of the same output columns.
+//
+// h_in is split between gridDim.z workgroups and their waves, each of which
+// reads U loads of each of its rows one batch ahead of the products.  x waits
+// in LDS: loads return in order, so x loaded in between would hold up W.
+template <WKind WK, int G, int CB, bool GLU>
 __global__ __launch_bounds__(kRowsThreads) void k_rows(RowsArgs a) {
   constexpr int F = RowsLoad<WK>::kFrags, KS = RowsLoad<WK>::kK;
   constexpr bool W4 = is_w4(WK);
   constexpr int NS = W4 ? 128 / G : 1;           // scales of one load
-  constexpr int U = W4 && G == 32 ? 2 : 4;       // loads of each row in flight, twice over
+  constexpr int U = 8 / F > 4 ? 4 : 8 / F;       // loads of a row in one batch
   constexpr int NP = GLU ? 2 : 1;
   constexpr int CPB = CB / NP;                   // column blocks
   union Shared {
-    RowsShrinkShared shrink;
-    f32x4 red[kRowsWaves][CB * TB][64];
+    RowsShrinkShared<1> shrink;
+    f32x4 red[kRowsWaves][CB][64];
+    unsigned char x[kRowsXBytes];
   };
   __shared__ Shared sh;
   const int tok0 = blockIdx.y * kRowsTokens, m = min(a.n - tok0, kRowsTokens);
   if (static_cast<int>(blockIdx.x) < a.n_units) {
-    rows_shrink(a, sh.shrink, blockIdx.x, NP, tok0, m);
+    if (blockIdx.z == 0) (void)rows_shrink<1>(a, sh.shrink, blockIdx.x, NP, tok0, m);
     return;
   }
   // consecutive column blocks on one XCD, so that they share lines of the scales in its L2
@@ -178,15 +403,13 @@ __global__ __launch_bounds__(kRowsThreads) void k_rows(RowsArgs a) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l16 = lane & 15, lq = lane >> 4;
   const int col0 = blk * (16 * CPB);
+  auto proj = [](int cb) { return GLU ? cb & 1 : 0; };
+  auto col = [&](int cb) { return col0 + 16 * (GLU ? cb >> 1 : cb); };
 
   const char* wp[CB];
 #pragma unroll
   for (int cb = 0; cb < CB; ++cb)
-    wp[cb] = static_cast<const char*>(a.w[GLU ? cb & 1 : 0].w) +
-             static_cast<int64_t>(col0 + 16 * (GLU ? cb >> 1 : cb) + l16) * a.ld_w;
-  const __bf16* xp[TB];
-#pragma unroll
-  for (int tb = 0; tb < TB; ++tb) xp[tb] = a.x + static_cast<int64_t>(tok0 + min(16 * tb + l16, m - 1)) * a.ld_x;
+    wp[cb] = static_cast<const char*>(a.w[proj(cb)].w) + static_cast<int64_t>(col(cb) + l16) * a.ld_w;
   W4Table tab[NP];
   if constexpr (WK == WKind::kTable4) {
 #pragma unroll
@@ -194,10 +417,16 @@ __global__ __launch_bounds__(kRowsThreads) void k_rows(RowsArgs a) {
   }
 
   const int steps = (a.h_in + KS - 1) / KS;
-  const int s0 = steps * wave / kRowsWaves, s1 = steps * (wave + 1) / kRowsWaves;
+  const int parts = kRowsWaves * gridDim.z, part = kRowsWaves * blockIdx.z + wave;
+  const int s0 = steps * part / parts, s1 = steps * (part + 1) / parts;
+  const int g0 = steps * (kRowsWaves * blockIdx.z) / parts;   // the workgroup's first step
   // a row's last load may reach past its end (h_in an odd multiple of 64 under
   // KS = 128): it is moved back into the row and x is zero there
   const int last = (W4 ? a.h_in / 2 : WK == WKind::kFp8 ? a.h_in : 2 * a.h_in) - 16;
+  // With one group to a 128-k load, the load's words meet the k that the lane
+  // itself holds (x is read at any offset); else the words are exchanged so
+  // that each product covers 32 consecutive k.
+  constexpr bool SWAP = W4 && G < 128;
 
   struct Batch {
     u32x4 w[U][CB];
@@ -217,8 +446,8 @@ __global__ __launch_bounds__(kRowsThreads) void k_rows(RowsArgs a) {
           const int g = min(su * NS + j, a.h_in / G - 1);
 #pragma unroll
           for (int cb = 0; cb < CB; ++cb) {
-            const WView& w = a.w[GLU ? cb & 1 : 0];
-            const int64_t o = g * w.ld_scale + col0 + 16 * (GLU ? cb >> 1 : cb) + 4 * lq;
+            const WView& w = a.w[proj(cb)];
+            const int64_t o = g * w.ld_scale + col(cb) + 4 * lq;
             t.s[u][j][cb] = *reinterpret_cast<const u32x2*>(static_cast<const __bf16*>(w.scale) + o);
             if (G < 128 && su * NS + j > g) t.s[u][j][cb] = u32x2{0u, 0u};   // past the last group
             t.z[u][j][cb] = 0x08080808u;
@@ -229,76 +458,45 @@ __global__ __launch_bounds__(kRowsThreads) void k_rows(RowsArgs a) {
     }
   };
 
-  f32x4 acc[CB][TB];
+  f32x4 acc[CB];
 #pragma unroll
-  for (int cb = 0; cb < CB; ++cb)
-#pragma unroll
-    for (int tb = 0; tb < TB; ++tb) acc[cb][tb] = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int cb = 0; cb < CB; ++cb) acc[cb] = f32x4{0.f, 0.f, 0.f, 0.f};
   const f32x4 none{0.f, 0.f, 0.f, 0.f};
   const bf16x8 ones = __builtin_bit_cast(bf16x8, u32x4{0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u});
+  const int x_row = rows_x_stride((steps * (kRowsWaves * (blockIdx.z + 1)) / parts - g0) * KS);   // bytes
 
   auto compute = [&](const Batch& t, int u, int s) {
-    // x of this load: F pieces of 8 k
-    bf16x8 xf[F][TB];
+    bf16x8 xf[F];
 #pragma unroll
     for (int f = 0; f < F; ++f) {
-      const int k = W4 ? s * KS + 32 * f + 8 * lq : s * KS + 8 * F * lq + 8 * f;
-#pragma unroll
-      for (int tb = 0; tb < TB; ++tb) {
-        if constexpr (W4) {
-          const bool in = k < a.h_in;
-          u32x4 v = *reinterpret_cast<const u32x4*>(xp[tb] + (in ? k : 0));
-          if (!in) v = u32x4{0u, 0u, 0u, 0u};
-          xf[f][tb] = __builtin_bit_cast(bf16x8, v);
-        } else {
-          xf[f][tb] = *reinterpret_cast<const bf16x8*>(xp[tb] + k);
-        }
-      }
+      const int k = SWAP ? 32 * f + 8 * lq : 8 * F * lq + 8 * f;
+      xf[f] = *reinterpret_cast<const bf16x8*>(sh.x + min(l16, m - 1) * x_row + 2 * ((s - g0) * KS + k));
     }
     if constexpr (!W4) {
 #pragma unroll
       for (int cb = 0; cb < CB; ++cb) {
         const u32x4 v = t.w[u][cb];
-        if constexpr (WK == WKind::kBf16) {
 #pragma unroll
-          for (int tb = 0; tb < TB; ++tb)
-            acc[cb][tb] = rows_mfma(__builtin_bit_cast(bf16x8, v), xf[0][tb], acc[cb][tb]);
-        } else {
-#pragma unroll
-          for (int f = 0; f < 2; ++f) {
-            u32x4 o;
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const bf16x2 lo = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v[2 * f + j], 1.0f, false);
-              const bf16x2 hi = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v[2 * f + j], 1.0f, true);
-              o[2 * j] = __builtin_bit_cast(uint32_t, lo);
-              o[2 * j + 1] = __builtin_bit_cast(uint32_t, hi);
-            }
-#pragma unroll
-            for (int tb = 0; tb < TB; ++tb)
-              acc[cb][tb] = rows_mfma(__builtin_bit_cast(bf16x8, o), xf[f][tb], acc[cb][tb]);
-          }
+        for (int f = 0; f < F; ++f) {
+          const bf16x8 wf = WK == WKind::kBf16 ? __builtin_bit_cast(bf16x8, v) : rows_fp8(v, f);
+          acc[cb] = rows_mfma(wf, xf[f], acc[cb]);
         }
       }
     } else {
-      f32x4 xs[NS][TB];   // sum of x over each group: every row of the product with ones
+      f32x4 xs[NS];   // sum of x over each group: every row of the product with ones
       if constexpr (WK == WKind::kInt4) {
 #pragma unroll
         for (int f = 0; f < 4; ++f)
-#pragma unroll
-          for (int tb = 0; tb < TB; ++tb)
-            xs[f * NS / 4][tb] = rows_mfma(ones, xf[f][tb], f % (4 / NS) == 0 ? none : xs[f * NS / 4][tb]);
+          xs[f * NS / 4] = rows_mfma(ones, xf[f], f % (4 / NS) == 0 ? none : xs[f * NS / 4]);
       }
 #pragma unroll
       for (int cb = 0; cb < CB; ++cb) {
-        const u32x4 v = rows_transpose4(t.w[u][cb]);
-        f32x4 sum[TB];
+        const u32x4 v = SWAP ? rows_transpose4(t.w[u][cb]) : t.w[u][cb];
+        f32x4 sum;
 #pragma unroll
         for (int f = 0; f < 4; ++f) {
-          const bf16x8 wf = w4_widen<WK>(v[f], tab[GLU ? cb & 1 : 0]);
-#pragma unroll
-          for (int tb = 0; tb < TB; ++tb)
-            sum[tb] = rows_mfma(wf, xf[f][tb], f % (4 / NS) == 0 ? none : sum[tb]);
+          const bf16x8 wf = w4_widen<WK, true>(v[f], tab[proj(cb)]);
+          sum = rows_mfma(wf, xf[f], f % (4 / NS) == 0 ? none : sum);
           if (f % (4 / NS) == 4 / NS - 1) {   // the group ends here: scale its sum
             const int j = f * NS / 4;
             const u32x2 s2 = t.s[u][j][cb];
@@ -307,10 +505,245 @@ __global__ __launch_bounds__(kRowsThreads) void k_rows(RowsArgs a) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const float z = static_cast<float>((zw >> (8 * e)) & 0xFFu);
+              float g = sum[e];
+              if constexpr (WK == WKind::kInt4) g = fmaf(-z, xs[j][0], g);
+              acc[cb][e] = fmaf(sc[e], g, acc[cb][e]);
+            }
+          }
+        }
+      }
+    }
+  };
+
+  Batch cur, nxt;
+  if (s0 < s1) load(cur, s0);
+  {
+    // x of the workgroup's k, in the order the widened codes come in; zero past h_in
+    const int k0 = g0 * KS, len = steps * (kRowsWaves * (blockIdx.z + 1)) / parts * KS - k0;
+    for (int i = threadIdx.x; i < m * (len >> 3); i += kRowsThreads) {
+      const int r = i / (len >> 3), k = 8 * (i - r * (len >> 3));
+      u32x4 v{0u, 0u, 0u, 0u};
+      if (k0 + k < a.h_in)
+        v = *reinterpret_cast<const u32x4*>(a.x + static_cast<int64_t>(tok0 + r) * a.ld_x + k0 + k);
+      if constexpr (WK == WKind::kInt4) v = w4_xl_order(v);
+      *reinterpret_cast<u32x4*>(sh.x + r * x_row + 2 * k) = v;
+    }
+    __syncthreads();
+  }
+  int s = s0;
+  for (; s + U <= s1; s += U) {
+    if (s + U < s1) load(nxt, s + U);
 #pragma unroll
-              for (int tb = 0; tb < TB; ++tb) {
-                float g = sum[tb][e];
-                if constexpr (WK == WKind::kInt4) g = fmaf(-z, xs[j][tb][0], g);
+    for (int u = 0; u < U; ++u) compute(cur, u, s + u);
+    cur = nxt;
+  }
+#pragma unroll
+  for (int u = 0; u < U - 1; ++u)
+    if (s + u < s1) compute(cur, u, s + u);
+
+  // ---- the waves' sums, in wave order
+  __syncthreads();   // x is read: its place is the sums'
+#pragma unroll
+  for (int cb = 0; cb < CB; ++cb) sh.red[wave][cb][lane] = acc[cb];
+  __syncthreads();
+  auto total = [&](int cb, int l) {
+    f32x4 v = sh.red[0][cb][l];
+#pragma unroll
+    for (int w = 1; w < kRowsWaves; ++w) v += sh.red[w][cb][l];
+    if constexpr (WK == WKind::kFp8)
+      v *= *reinterpret_cast<const f32x4*>(static_cast<const float*>(a.w[proj(cb)].scale) + col(cb) + 4 * (l >> 4));
+    return v;
+  };
+  if (a.part) {
+    for (int it = threadIdx.x; it < CB * 64; it += kRowsThreads) {
+      const int cb = it >> 6, l = it & 63, tok = l & 15;
+      if (tok < m) rows_put_part(a, NP, proj(cb), tok0 + tok, col(cb) + 4 * (l >> 4), total(cb, l));
+    }
+  } else {
+    for (int it = threadIdx.x; it < CPB * 64; it += kRowsThreads) {
+      const int cp = it >> 6, l = it & 63, tok = l & 15;
+      if (tok < m)
+        rows_put<GLU>(a, tok0 + tok, col0 + 16 * cp + 4 * (l >> 4), total(NP * cp, l), total(NP * cp + NP - 1, l));
+    }
+  }
+}
+
+// More tokens: 16 * TB of them and 8 waves of CB 16-row blocks each.  The
+// waves share x, 128 k at a time through two LDS buffers, so that its reads
+// from L2 (two bytes a token and k for every workgroup) stay below W's; each
+// wave reads its own rows of W straight into registers.  Both run D - 1 steps
+// ahead.  With GLU half of a wave's blocks are gate rows and half up rows.
+//
+// x in LDS: rows of 256 bytes whose 16-byte chunks are XORed with the row, so
+// that the 16 rows of a fragment read cover all banks once.  The sums of x over
+// each group, which a zero point multiplies, are formed on the way in.
+template <WKind WK, int G, int TB, int CB, bool GLU>
+__global__ __launch_bounds__(kRowsThreads) void k_mid(RowsArgs a) {
+  constexpr int F = RowsLoad<WK>::kFrags, KS = 128;
+  constexpr bool W4 = is_w4(WK), Z = WK == WKind::kInt4;
+  constexpr int L = 4 / F;                       // loads of a row in one step
+  constexpr int NS = W4 ? 128 / G : 1;           // scales of one step
+  constexpr int D = WK == WKind::kBf16 ? 2 : 3;  // steps in registers
+  constexpr int NP = GLU ? 2 : 1;
+  constexpr int XP = TB == 4 ? 2 : 1;            // 16-byte pieces of x a thread moves in one step
+  struct Stage {
+    alignas(16) unsigned char x[16 * TB * 256];
+    float xs[Z ? NS : 1][Z ? 16 * TB : 1];
+  };
+  union Shared {
+    RowsShrinkShared<TB> shrink;
+    Stage st[2];
+  };
+  __shared__ Shared sh;
+  const int tok0 = blockIdx.y * 16 * TB, m = min(a.n - tok0, 16 * TB);
+  if (static_cast<int>(blockIdx.x) < a.n_units) {
+    if (blockIdx.z == 0) (void)rows_shrink<TB>(a, sh.shrink, blockIdx.x, NP, tok0, m);
+    return;
+  }
+  const int b = blockIdx.x - a.n_units, per = (a.n_blocks + 7) >> 3;
+  const int blk = (b & 7) * per + (b >> 3);
+  if (blk >= a.n_blocks) return;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int l16 = lane & 15, lq = lane >> 4;
+  const int col0 = (blk * kRowsWaves + wave) * (16 * CB / NP);   // may start past h_out: such a wave only moves x
+  auto proj = [](int cb) { return GLU ? cb & 1 : 0; };
+  auto col = [&](int cb) { return col0 + 16 * (GLU ? cb >> 1 : cb); };
+
+  const char* wp[CB];
+#pragma unroll
+  for (int cb = 0; cb < CB; ++cb)
+    wp[cb] = static_cast<const char*>(a.w[proj(cb)].w) + static_cast<int64_t>(min(col(cb), a.h_out - 16) + l16) * a.ld_w;
+  W4Table tab[NP];
+  if constexpr (WK == WKind::kTable4) {
+#pragma unroll
+    for (int p = 0; p < NP; ++p) tab[p].load(a.w[p].table);
+  }
+  const int steps = (a.h_in + KS - 1) / KS, parts = gridDim.z;
+  const int s0 = steps * blockIdx.z / parts, s1 = steps * (blockIdx.z + 1) / parts;
+  // a row's last load may reach past its end (h_in an odd multiple of 64): it
+  // is moved back into the row and x is zero there
+  const int row_bytes = W4 ? a.h_in / 2 : WK == WKind::kFp8 ? a.h_in : 2 * a.h_in;
+
+  // piece q of this thread: row xrow, chunk xchunk of the step's x
+  const __bf16* xsrc[XP];
+  int xdst[XP];
+  const int xchunk = tid & 15;
+#pragma unroll
+  for (int q = 0; q < XP; ++q) {
+    const int r = ((tid >> 4) + 32 * q) % (16 * TB);
+    xsrc[q] = a.x + static_cast<int64_t>(tok0 + min(r, m - 1)) * a.ld_x;
+    xdst[q] = r * 256 + ((xchunk ^ (r & 15)) << 4);
+  }
+  struct Step {
+    u32x4 w[L][CB];
+    u32x4 x[XP];
+    u32x2 s[NS][W4 ? CB : 1];
+    uint32_t z[NS][Z ? CB : 1];
+  };
+  auto load_w = [&](Step& t, int s) {
+    s = min(s, s1 - 1);
+#pragma unroll
+    for (int l = 0; l < L; ++l)
+#pragma unroll
+      for (int cb = 0; cb < CB; ++cb)
+        t.w[l][cb] = ld16<true>(
+            reinterpret_cast<const u32x4*>(wp[cb] + min(s * (64 * L) + 64 * l + 16 * lq, row_bytes - 16)));
+    if constexpr (W4) {
+#pragma unroll
+      for (int j = 0; j < NS; ++j) {
+        const int g = min(s * NS + j, a.h_in / G - 1);
+#pragma unroll
+        for (int cb = 0; cb < CB; ++cb) {
+          const WView& w = a.w[proj(cb)];
+          const int64_t o = g * w.ld_scale + min(col(cb), a.h_out - 16) + 4 * lq;
+          t.s[j][cb] = *reinterpret_cast<const u32x2*>(static_cast<const __bf16*>(w.scale) + o);
+          if (G < 128 && s * NS + j > g) t.s[j][cb] = u32x2{0u, 0u};   // past the last group
+          if constexpr (Z) {
+            t.z[j][cb] = 0x08080808u;
+            if (w.zero) t.z[j][cb] = *reinterpret_cast<const uint32_t*>(w.zero + o);
+          }
+        }
+      }
+    }
+  };
+  auto load_x = [&](Step& t, int s) {
+    const int k = min(s, s1 - 1) * KS + 8 * xchunk;
+#pragma unroll
+    for (int q = 0; q < XP; ++q) t.x[q] = *reinterpret_cast<const u32x4*>(xsrc[q] + (k < a.h_in ? k : 0));
+  };
+  auto store_x = [&](const Step& t, int s, Stage& st) {
+#pragma unroll
+    for (int q = 0; q < XP; ++q) {
+      u32x4 v = t.x[q];
+      if (s * KS + 8 * xchunk >= a.h_in) v = u32x4{0u, 0u, 0u, 0u};
+      *reinterpret_cast<u32x4*>(st.x + xdst[q]) = v;   // threads past a small tile write what others do
+      if constexpr (Z) {
+        float f = ((bf16lo(v.x) + bf16hi(v.x)) + (bf16lo(v.y) + bf16hi(v.y))) +
+                  ((bf16lo(v.z) + bf16hi(v.z)) + (bf16lo(v.w) + bf16hi(v.w)));
+        f += xor_lane<1>(f);
+        f += xor_lane<2>(f);
+        if constexpr (G >= 64) f += xor_lane<4>(f);
+        if constexpr (G >= 128) f += xor_lane<8>(f);
+        if ((xchunk & (G / 8 - 1)) == 0) st.xs[xchunk / (G / 8)][xdst[q] >> 8] = f;
+      }
+    }
+  };
+
+  f32x4 acc[CB][TB];
+#pragma unroll
+  for (int cb = 0; cb < CB; ++cb)
+#pragma unroll
+    for (int tb = 0; tb < TB; ++tb) acc[cb][tb] = f32x4{0.f, 0.f, 0.f, 0.f};
+  const f32x4 none{0.f, 0.f, 0.f, 0.f};
+
+  auto compute = [&](const Step& t, const Stage& st) {
+    auto x_at = [&](int tb, int chunk) {
+      return *reinterpret_cast<const bf16x8*>(st.x + (16 * tb + l16) * 256 + ((chunk ^ l16) << 4));
+    };
+    if constexpr (!W4) {
+#pragma unroll
+      for (int f = 0; f < 4; ++f) {
+        bf16x8 wf[CB];
+#pragma unroll
+        for (int cb = 0; cb < CB; ++cb)
+          wf[cb] = WK == WKind::kBf16 ? __builtin_bit_cast(bf16x8, t.w[f / F][cb]) : rows_fp8(t.w[f / F][cb], f % F);
+#pragma unroll
+        for (int tb = 0; tb < TB; ++tb) {
+          const bf16x8 xf = x_at(tb, WK == WKind::kBf16 ? 4 * f + lq : 8 * (f >> 1) + 2 * lq + (f & 1));
+#pragma unroll
+          for (int cb = 0; cb < CB; ++cb) acc[cb][tb] = rows_mfma(wf[cb], xf, acc[cb][tb]);
+        }
+      }
+    } else {
+      u32x4 v[CB];
+#pragma unroll
+      for (int cb = 0; cb < CB; ++cb) v[cb] = rows_transpose4(t.w[0][cb]);
+      f32x4 sum[CB][TB];
+#pragma unroll
+      for (int f = 0; f < 4; ++f) {
+        bf16x8 wf[CB];
+#pragma unroll
+        for (int cb = 0; cb < CB; ++cb) wf[cb] = w4_widen<WK>(v[cb][f], tab[proj(cb)]);
+#pragma unroll
+        for (int tb = 0; tb < TB; ++tb) {
+          const bf16x8 xf = x_at(tb, 4 * f + lq);
+#pragma unroll
+          for (int cb = 0; cb < CB; ++cb)
+            sum[cb][tb] = rows_mfma(wf[cb], xf, f % (4 / NS) == 0 ? none : sum[cb][tb]);
+        }
+        if (f % (4 / NS) == 4 / NS - 1) {   // the group ends here: scale its sum
+          const int j = f * NS / 4;
+#pragma unroll
+          for (int tb = 0; tb < TB; ++tb) {
+            const float xs = Z ? st.xs[j][16 * tb + l16] : 0.f;
+#pragma unroll
+            for (int cb = 0; cb < CB; ++cb) {
+              const u32x2 s2 = t.s[j][cb];
+              const f32x4 sc{bf16lo(s2.x), bf16hi(s2.x), bf16lo(s2.y), bf16hi(s2.y)};
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                float g = sum[cb][tb][e];
+                if constexpr (Z) g = fmaf(-static_cast<float>((t.z[j][cb] >> (8 * e)) & 0xFFu), xs, g);
                 acc[cb][tb][e] = fmaf(sc[e], g, acc[cb][tb][e]);
               }
             }
@@ -320,60 +753,45 @@ __global__ __launch_bounds__(kRowsThreads) void k_rows(RowsArgs a) {
     }
   };
 
-  if (s0 < s1) {
-    Batch cur, nxt;
-    load(cur, s0);
-    for (int s = s0; s < s1; s += U) {
-      if (s + U < s1) load(nxt, s + U);
+  // step s computes on ring slot s % D while its x is in LDS buffer s % 2; x
+  // of step s + 1 goes to the other buffer, whose readers passed the barrier
+  Step ring[D];
 #pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (s + u < s1) compute(cur, u, s + u);
-      cur = nxt;
+  for (int d = 0; d < D - 1; ++d) {
+    load_x(ring[d], s0 + d);
+    load_w(ring[d], s0 + d);
+  }
+  store_x(ring[0], s0, sh.st[0]);
+  for (int s = s0; s < s1; s += 2 * D) {
+#pragma unroll
+    for (int i = 0; i < 2 * D; ++i) {
+      if (s + i >= s1) break;
+      __syncthreads();
+      load_x(ring[(i + D - 1) % D], s + i + D - 1);
+      load_w(ring[(i + D - 1) % D], s + i + D - 1);
+      compute(ring[i % D], sh.st[i & 1]);
+      if (s + i + 1 < s1) store_x(ring[(i + 1) % D], s + i + 1, sh.st[(i + 1) & 1]);
     }
   }
 
-  // ---- the waves' sums, in wave order
 #pragma unroll
   for (int cb = 0; cb < CB; ++cb)
-#pragma unroll
-    for (int tb = 0; tb < TB; ++tb) sh.red[wave][cb * TB + tb][lane] = acc[cb][tb];
-  __syncthreads();
-  auto total = [&](int cb, int tb, int l) {
-    f32x4 v = sh.red[0][cb * TB + tb][l];
-#pragma unroll
-    for (int w = 1; w < kRowsWaves; ++w) v += sh.red[w][cb * TB + tb][l];
     if constexpr (WK == WKind::kFp8) {
-      const int c = col0 + 16 * (GLU ? cb >> 1 : cb) + 4 * (l >> 4);
-      v *= *reinterpret_cast<const f32x4*>(static_cast<const float*>(a.w[GLU ? cb & 1 : 0].scale) + c);
-    }
-    return v;
-  };
-  if (a.part) {
-    for (int it = threadIdx.x; it < CB * TB * 64; it += kRowsThreads) {
-      const int cb = it / (TB * 64), tb = (it >> 6) % TB, l = it & 63;
-      const int tok = 16 * tb + (l & 15), c = col0 + 16 * (GLU ? cb >> 1 : cb) + 4 * (l >> 4);
-      if (tok < m) {
-        float* to = a.part + (static_cast<int64_t>(GLU ? cb & 1 : 0) * a.n + tok0 + tok) * a.h_out + c;
-        *reinterpret_cast<f32x4*>(to) = total(cb, tb, l);
-      }
-    }
-  } else {
-    for (int it = threadIdx.x; it < CPB * TB * 64; it += kRowsThreads) {
-      const int cp = it / (TB * 64), tb = (it >> 6) % TB, l = it & 63;
-      const int tok = 16 * tb + (l & 15), c = col0 + 16 * cp + 4 * (l >> 4);
-      if (tok < m) {
-        f32x4 v = total(GLU ? 2 * cp : cp, tb, l);
-        if constexpr (GLU) {
-          const f32x4 up = total(2 * cp + 1, tb, l);
+      const f32x4 sc = *reinterpret_cast<const f32x4*>(static_cast<const float*>(a.w[proj(cb)].scale) +
+                                                       min(col(cb), a.h_out - 16) + 4 * lq);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) v[e] = glu_act(a.act, v[e]) * up[e];
-        }
-        __bf16 o[4];
+      for (int tb = 0; tb < TB; ++tb) acc[cb][tb] *= sc;
+    }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o[e] = static_cast<__bf16>(v[e]);
-        *reinterpret_cast<u32x2*>(a.y + (tok0 + static_cast<int64_t>(tok)) * a.ld_y + c) =
-            __builtin_bit_cast(u32x2, o);
-      }
+  for (int tb = 0; tb < TB; ++tb) {
+    const int tok = 16 * tb + l16;
+    if (tok >= m) continue;
+#pragma unroll
+    for (int cb = 0; cb < CB; ++cb) {
+      const int c = col(cb) + 4 * lq;
+      if (c >= a.h_out) continue;
+      if (a.part) rows_put_part(a, NP, proj(cb), tok0 + tok, c, acc[cb][tb]);
+      else if (!GLU || proj(cb) == 0) rows_put<GLU>(a, tok0 + tok, c, acc[cb][tb], acc[cb + NP - 1][tb]);
     }
   }
 }
@@ -387,11 +805,15 @@ __global__ __launch_bounds__(kFinishThreads) void k_rows_finish(RowsArgs a) {
   const int tok = blockIdx.y;
   const int c = 4 * (blockIdx.x * kFinishThreads + threadIdx.x);
   if (c >= a.h_out) return;
-  const int id = a.ids[tok];
+  const int id = a.ids ? a.ids[tok] : -1;
   f32x4 v[NP];
 #pragma unroll
   for (int p = 0; p < NP; ++p)
     v[p] = *reinterpret_cast<const f32x4*>(a.part + (static_cast<int64_t>(p) * a.n + tok) * a.h_out + c);
+  for (int z = 1; z < a.splits; ++z)
+#pragma unroll
+    for (int p = 0; p < NP; ++p)
+      v[p] += *reinterpret_cast<const f32x4*>(a.part + (static_cast<int64_t>(z * NP + p) * a.n + tok) * a.h_out + c);
   if (id >= 0 && id < a.pv.n_slots) {
     const int h = static_cast<int>(a.pv.page_elems), ppr = a.h_out / h;
     const int cp = c / h, off = c - cp * h;

@@ -9,8 +9,8 @@ namespace {
 template <WKind WK, bool GLU, bool G32>
 void launch(const FusedArgs& a, hipStream_t s) {
   const dim3 grid(static_cast<unsigned>((a.n_tiles + 7) / 8 * 8));
-  if (a.ids) hipLaunchKernelGGL((k_fused_gemm<true, WK, GLU, G32>), grid, dim3(kFgThreads), 0, s, a);
-  else hipLaunchKernelGGL((k_fused_gemm<false, WK, GLU, G32>), grid, dim3(kFgThreads), 0, s, a);
+  if (a.ids) hipLaunchKernelGGL((k_fused_gemm<FgLora::kGiven, WK, GLU, G32>), grid, dim3(kFgThreads), 0, s, a);
+  else hipLaunchKernelGGL((k_fused_gemm<FgLora::kNone, WK, GLU, G32>), grid, dim3(kFgThreads), 0, s, a);
 }
 
 template <WKind WK, bool GLU>
@@ -29,6 +29,8 @@ lora_status launch_tiles(const BaseCall& c, hipStream_t s) {
   a.w[1] = c.w[1];
   a.ids = c.ids;
   a.y = c.y;
+  a.t = c.ids ? c.ws : nullptr;
+  a.t_splits = tiles_splits(c.n, c.h_in);
   a.ld_x = c.ld_x;
   a.ld_w = c.ld_w;
   a.ld_y = c.ld_y;
