@@ -1,6 +1,8 @@
 // C ABI of the base products with 4-bit weights and of the gated feed-forward
 // product: argument checks and path selection.
 #include <algorithm>
+#include <utility>
+#include <cstdlib>
 
 #include "base_launch.hpp"
 #include "fused_gemm.hpp"
@@ -10,16 +12,9 @@ using namespace lora;
 
 namespace {
 
-// Batches up to this many tokens stream W's rows (rows_kernels.hpp), longer
-// ones take tiles of 256 tokens (fused_gemm.hpp).
-constexpr int32_t kRowsMaxTokens = 64;
-
-bool takes_rows(int32_t n_tokens) { return n_tokens <= kRowsMaxTokens; }
-
 // Workspace that a call with ids needs at least (a shorter one only limits the split of h_in).
-size_t ws_need(int n_proj, int32_t n_tokens, int64_t h_in, int64_t h_out) {
-  return takes_rows(n_tokens) ? rows_bytes(1, n_proj, n_tokens, h_out)
-                              : tiles_ws_bytes(n_proj, n_tokens, static_cast<int32_t>(h_in));
+size_t ws_need(bool rows, int n_proj, int32_t n_tokens, int64_t h_in, int64_t h_out) {
+  return rows ? rows_bytes(1, n_proj, n_tokens, h_out) : tiles_ws_bytes(n_proj, n_tokens, static_cast<int32_t>(h_in));
 }
 
 bool aligned(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
@@ -70,8 +65,11 @@ lora_status base_call(const lora_pool* p, BaseCall& c, const int32_t* module, co
   const int n_proj = c.glu ? 2 : 1;
   const int64_t h_out = p->h_out[module[0]];
   if (ws_bytes > 0 && (!ws || !aligned(ws, 16))) return LORA_ERR_ARG;
-  if (ids && ws_bytes < ws_need(n_proj, n_tokens, p->h_in[module[0]], h_out)) return LORA_ERR_WORKSPACE;
   if (n_tokens == 0) return LORA_OK;
+  const int64_t h_in = p->h_in[module[0]];
+  const bool rows = rows_faster(c.kind, c.group, n_proj, n_tokens, static_cast<int32_t>(h_in),
+                                static_cast<int32_t>(h_out));
+  if (ids && ws_bytes < ws_need(rows, n_proj, n_tokens, h_in, h_out)) return LORA_ERR_WORKSPACE;
   DeviceGuard g(p->device);
   if (!g.ok) return LORA_ERR_HIP;
   c.pv = p->view();
@@ -81,14 +79,14 @@ lora_status base_call(const lora_pool* p, BaseCall& c, const int32_t* module, co
   c.ld_x = ld_x;
   c.ld_y = ld_y;
   c.n = n_tokens;
-  c.h_in = static_cast<int32_t>(p->h_in[module[0]]);
+  c.h_in = static_cast<int32_t>(h_in);
   c.h_out = static_cast<int32_t>(h_out);
   c.module[0] = module[0];
   c.module[1] = module[n_proj - 1];
   c.ws = static_cast<float*>(ws);
   c.ws_bytes = ws_bytes;
   hipStream_t s = static_cast<hipStream_t>(stream);
-  if (takes_rows(n_tokens)) return launch_rows(c, s);
+  if (rows) return launch_rows(c, s);
   if (ids) {
     const lora_status st = launch_shrink(c, tiles_splits(c.n, c.h_in), s);
     if (st != LORA_OK) return st;
@@ -104,11 +102,13 @@ extern "C" {
 
 size_t lora_fused_workspace_bytes(const lora_pool* p, int32_t module, int32_t n_proj, int32_t n_tokens) {
   if (!p || module < 0 || module >= p->n_modules || n_proj < 1 || n_proj > 2 || n_tokens < 1) return 0;
-  if (!takes_rows(n_tokens)) return tiles_ws_bytes(n_proj, n_tokens, static_cast<int32_t>(p->h_in[module]));
-  size_t most = 0;
-  for (WKind k : {WKind::kBf16, WKind::kFp8, WKind::kInt4})
-    most = std::max(most, rows_ws_bytes(k, n_proj, n_tokens, static_cast<int32_t>(p->h_in[module]),
-                                        static_cast<int32_t>(p->h_out[module])));
+  const int32_t h_in = static_cast<int32_t>(p->h_in[module]), h_out = static_cast<int32_t>(p->h_out[module]);
+  size_t most = 0;   // over the kinds of weights, as the call is not known
+  for (const auto& [kind, group] : {std::pair{WKind::kBf16, 0}, std::pair{WKind::kFp8, 0}, std::pair{WKind::kInt4, 32},
+                                    std::pair{WKind::kInt4, 128}})
+    most = std::max(most, rows_faster(kind, group, n_proj, n_tokens, h_in, h_out)
+                              ? rows_ws_bytes(kind, group, n_proj, n_tokens, h_in, h_out)
+                              : tiles_ws_bytes(n_proj, n_tokens, h_in));
   return most;
 }
 

@@ -7,10 +7,10 @@
 namespace lora {
 namespace {
 
-constexpr int kRowsCB = 2;   // 16-row blocks of W^T to a wave
+constexpr int kRowsCB = 2;   // 16-row blocks of W^T to a wave of k_rows
 
 struct RowsPlan {
-  int tb;        // 16-token blocks of a workgroup: 1, 2 or 4
+  int tb;        // 16-token blocks of a workgroup: 1 to 4
   bool x_lds;    // k_rows, else k_mid
   int blocks;    // base workgroups of one split and chunk
   int chunks;    // of 16 * tb tokens
@@ -20,9 +20,12 @@ struct RowsPlan {
 // Base workgroups that a split of h_in aims at.
 constexpr int kRowsWgTarget = 256;
 
-RowsPlan rows_plan(WKind kind, int n_proj, int32_t n, int32_t h_in, int32_t h_out, size_t ws_bytes) {
+RowsPlan rows_plan(WKind kind, int group, int n_proj, int32_t n, int32_t h_in, int32_t h_out, size_t ws_bytes) {
   RowsPlan p{};
-  p.tb = n <= 16 ? 1 : n <= 32 ? 2 : 4;
+  // with groups of 32 the scales of a step leave registers for 32 tokens only
+  // (64 tokens, 4160 -> 5440: 83 us with 64 at a time and spills, XX us with 32)
+  const int most = is_w4(kind) && group == 32 ? 2 : 4;
+  p.tb = n > 16 * most ? most : (n + 15) / 16;
   p.chunks = (n + 16 * p.tb - 1) / (16 * p.tb);
   auto split = [&](int cols, int steps, int min_steps) {
     p.blocks = (h_out * n_proj + cols - 1) / cols;
@@ -35,7 +38,7 @@ RowsPlan rows_plan(WKind kind, int n_proj, int32_t n, int32_t h_in, int32_t h_ou
     const int range = ((steps + p.splits - 1) / p.splits + 1) * ks;   // at most, of one workgroup
     p.x_lds = n * rows_x_stride(range) <= kRowsXBytes;
   }
-  if (!p.x_lds) split(16 * kRowsCB * kRowsWaves, (h_in + 127) / 128, 2);
+  if (!p.x_lds) split(32 * kMidWaves, (h_in + 127) / 128, 2);
   return p;
 }
 
@@ -43,11 +46,15 @@ template <WKind WK, int G, bool GLU>
 void by_tokens(const RowsArgs& base, const RowsPlan& p, hipStream_t s) {
   RowsArgs a = base;
   a.n_blocks = p.blocks;
-  const dim3 grid(static_cast<unsigned>(a.n_units + (a.n_blocks + 7) / 8 * 8), p.chunks, p.splits), wg(kRowsThreads);
+  const dim3 grid(static_cast<unsigned>((a.n_units + (a.n_blocks + 7) / 8 * 8) * p.chunks), 1, p.splits);
+  const dim3 wg(kRowsThreads), wg_mid(kMidThreads);
   if (p.x_lds) hipLaunchKernelGGL((k_rows<WK, G, kRowsCB, GLU>), grid, wg, 0, s, a);
-  else if (p.tb == 1) hipLaunchKernelGGL((k_mid<WK, G, 1, kRowsCB, GLU>), grid, wg, 0, s, a);
-  else if (p.tb == 2) hipLaunchKernelGGL((k_mid<WK, G, 2, kRowsCB, GLU>), grid, wg, 0, s, a);
-  else hipLaunchKernelGGL((k_mid<WK, G, 4, kRowsCB, GLU>), grid, wg, 0, s, a);
+  else if (p.tb == 1) hipLaunchKernelGGL((k_mid<WK, G, 1, GLU>), grid, wg_mid, 0, s, a);
+  else if (p.tb == 2) hipLaunchKernelGGL((k_mid<WK, G, 2, GLU>), grid, wg_mid, 0, s, a);
+  else if constexpr (G != 32) {
+    if (p.tb == 3) hipLaunchKernelGGL((k_mid<WK, G, 3, GLU>), grid, wg_mid, 0, s, a);
+    else hipLaunchKernelGGL((k_mid<WK, G, 4, GLU>), grid, wg_mid, 0, s, a);
+  }
 }
 
 template <WKind WK, bool GLU>
@@ -79,8 +86,25 @@ RowsArgs rows_args(const BaseCall& c) {
 
 }  // namespace
 
-size_t rows_ws_bytes(WKind kind, int n_proj, int32_t n, int32_t h_in, int32_t h_out) {
-  return rows_bytes(rows_plan(kind, n_proj, n, h_in, h_out, SIZE_MAX).splits, n_proj, n, h_out);
+// Which kernels are faster, from their measured costs in microseconds.  Rows: 10
+// to start, 0.45 for each 10^6 weights and chunk of 64 tokens, 6 for each 10^6
+// base sums written and read.  Tiles: 35 to start (with the shrink) and 0.032 for each k of every
+// round of 256 tiles.  Measured, rows against tiles: 4096x4096 4-bit 67 / 154 at
+// 512 tokens, 118 / 157 at 1024; 4096 -> 2 x 12288 bf16 113 / 154 at 128, 206 /
+// 128 at 256; 768 -> 2 x 2304 4-bit 45 / 60 at 512, 83 / 62 at 1024; 2048 ->
+// 2 x 8192 fp8, ranks up to 64, 83 / 143 at 256, 154 / 144 at 512.
+bool rows_faster(WKind kind, int group, int n_proj, int32_t n, int32_t h_in, int32_t h_out) {
+  if (n <= 64) return true;
+  const double cols = static_cast<double>(n_proj) * h_out;
+  const double rows = 10.0 + 0.45e-6 * cols * h_in * ((n + 63) / 64) * (is_w4(kind) && group == 32 ? 1.5 : 1.0) +
+                      6e-6 * n * cols;
+  const double n_tiles = ((static_cast<double>(n) + 255) / 256) * ((cols + 255) / 256);
+  const double rounds = static_cast<double>(static_cast<int64_t>((n_tiles + 255) / 256));
+  return rows < 35.0 + 0.032 * h_in * rounds;
+}
+
+size_t rows_ws_bytes(WKind kind, int group, int n_proj, int32_t n, int32_t h_in, int32_t h_out) {
+  return rows_bytes(rows_plan(kind, group, n_proj, n, h_in, h_out, SIZE_MAX).splits, n_proj, n, h_out);
 }
 
 lora_status launch_shrink(const BaseCall& c, int splits, hipStream_t s) {
@@ -94,7 +118,7 @@ lora_status launch_shrink(const BaseCall& c, int splits, hipStream_t s) {
 lora_status launch_rows(const BaseCall& c, hipStream_t s) {
   RowsArgs a = rows_args(c);
   const int n_proj = c.glu ? 2 : 1;
-  const RowsPlan p = rows_plan(c.kind, n_proj, c.n, c.h_in, c.h_out, c.ws_bytes);
+  const RowsPlan p = rows_plan(c.kind, c.group, n_proj, c.n, c.h_in, c.h_out, c.ws_bytes);
   a.splits = p.splits;
   if (c.ids || p.splits > 1) a.part = c.ws;
   if (c.ids) {
@@ -116,7 +140,7 @@ lora_status launch_rows(const BaseCall& c, hipStream_t s) {
   }
   if (hipGetLastError() != hipSuccess) return LORA_ERR_HIP;
   if (a.part) {
-    const dim3 grid((c.h_out / 4 + kFinishThreads - 1) / kFinishThreads, c.n);
+    const dim3 grid((c.h_out + kFinishCols - 1) / kFinishCols, c.n);
     if (c.glu) hipLaunchKernelGGL((k_rows_finish<true>), grid, dim3(kFinishThreads), 0, s, a);
     else hipLaunchKernelGGL((k_rows_finish<false>), grid, dim3(kFinishThreads), 0, s, a);
   }

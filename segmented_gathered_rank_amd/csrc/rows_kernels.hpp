@@ -32,6 +32,9 @@ namespace lora {
 
 constexpr int kRowsWaves = 8;
 constexpr int kRowsThreads = 64 * kRowsWaves;
+constexpr int kMidWaves = 8;       // waves of k_mid that multiply
+constexpr int kMidMovers = 4;      // and that bring x
+constexpr int kMidThreads = 64 * (kMidWaves + kMidMovers);
 constexpr int kRowsTokens = 64;    // tokens of one workgroup; longer batches run as chunks of this many
 constexpr int kRowsMaxPpr = 32;    // A pages per rank row
 constexpr int kRowsTRow = kMaxRank;
@@ -69,6 +72,20 @@ __device__ __forceinline__ f32x4 rows_mfma(bf16x8 a, bf16x8 b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
 
+// Loads written before this are issued before what follows: the compiler would
+// otherwise move them down to their first use.
+__device__ __forceinline__ void rows_issue() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+}
+
+// Where the zero points are read: where there are none, from the scales (twice
+// their bytes), and not used.  A load under a condition would make every step
+// wait for the loads before it, as the other side writes the same register.
+__device__ __forceinline__ const uint8_t* rows_zeros(const WView& w) {
+  return w.zero ? w.zero : static_cast<const uint8_t*>(w.scale);
+}
+
 // Word f of lane group q becomes word q of lane group f.
 __device__ __forceinline__ u32x4 rows_transpose4(u32x4 v) {
   const auto a = __builtin_amdgcn_permlane32_swap(v.x, v.z, false, false);
@@ -92,23 +109,23 @@ __device__ __forceinline__ bool rows_distinct(int mine, bool valid, int d, int* 
   return false;
 }
 
-template <int T>   // 16-token blocks a pass over K takes at most
+template <int T, int NW>   // 16-token blocks a pass over K takes at most, waves
 struct RowsShrinkShared {
   int32_t pid[16][kRowsMaxPpr];
   int32_t tok[kRowsTokens];
-  f32x4 red[kRowsWaves][T][64];
+  f32x4 red[NW][T][64];
 };
 
 // t of one 16-row block of adapter e for the n_tok tokens listed in sh.tok.
-template <int T, int TM>
-__device__ __forceinline__ void rows_shrink_block(const RowsArgs& a, RowsShrinkShared<TM>& sh, const SlotEntry& e,
+template <int T, int TM, int NW>
+__device__ __forceinline__ void rows_shrink_block(const RowsArgs& a, RowsShrinkShared<TM, NW>& sh, const SlotEntry& e,
                                                   int p, int rb, int tok0, int n_tok, int lane, int wave) {
   constexpr int U = T == 1 ? 8 : 4;
   const int l16 = lane & 15, lq = lane >> 4;
   const int h = static_cast<int>(a.pv.page_elems);
   const __bf16* pages = static_cast<const __bf16*>(a.pv.pages);
   const int n32 = a.h_in >> 5;
-  const int s0 = n32 * wave / kRowsWaves, s1 = n32 * (wave + 1) / kRowsWaves;
+  const int s0 = n32 * wave / NW, s1 = n32 * (wave + 1) / NW;
   int tok[T];
   const __bf16* xr[T];
   f32x4 acc[T];
@@ -151,7 +168,7 @@ __device__ __forceinline__ void rows_shrink_block(const RowsArgs& a, RowsShrinkS
     if (wave != tb || 16 * tb + l16 >= n_tok) continue;
     f32x4 v = sh.red[0][tb][lane];
 #pragma unroll
-    for (int w = 1; w < kRowsWaves; ++w) v += sh.red[w][tb][lane];
+    for (int w = 1; w < NW; ++w) v += sh.red[w][tb][lane];
     float* to = a.t + (static_cast<int64_t>(p) * a.n + tok0 + tok[tb]) * kRowsTRow + 16 * rb + 4 * lq;
     *reinterpret_cast<f32x4*>(to) = v * e.scale;
   }
@@ -160,8 +177,8 @@ __device__ __forceinline__ void rows_shrink_block(const RowsArgs& a, RowsShrinkS
 // Shrink unit `unit` of the chunk of tokens tok0 .. tok0 + m - 1: (distinct
 // adapter, projection, 16-row block).  Whole workgroup; false when the chunk
 // has no such adapter (nor any later one).
-template <int TM>
-__device__ __forceinline__ bool rows_shrink(const RowsArgs& a, RowsShrinkShared<TM>& sh, int unit, int n_proj,
+template <int TM, int NW>
+__device__ __forceinline__ bool rows_shrink(const RowsArgs& a, RowsShrinkShared<TM, NW>& sh, int unit, int n_proj,
                                             int tok0, int m) {
   // uniform: the matrix instructions ignore the execution mask, so what they
   // depend on must be a branch of the whole wave
@@ -178,13 +195,13 @@ __device__ __forceinline__ bool rows_shrink(const RowsArgs& a, RowsShrinkShared<
   const int n_tok = __popcll(same);
   if (wave == 0 && (same >> lane & 1)) sh.tok[__popcll(same & ((uint64_t(1) << lane) - 1))] = lane;
   const int ppr = a.h_in / static_cast<int>(a.pv.page_elems);
-  for (int q = threadIdx.x; q < 16 * ppr; q += kRowsThreads) {
+  for (int q = threadIdx.x; q < 16 * ppr; q += 64 * NW) {
     const int r = q / ppr, kp = q - r * ppr, j = 16 * rb + r;
     sh.pid[r][kp] = j < e.rank ? a.pv.page_ids[e.a_off + j * ppr + kp] : a.pv.zero_page;
   }
   __syncthreads();
-  if (TM == 1 || n_tok <= 16) rows_shrink_block<1, TM>(a, sh, e, p, rb, tok0, n_tok, lane, wave);
-  else rows_shrink_block<TM, TM>(a, sh, e, p, rb, tok0, n_tok, lane, wave);
+  if (TM == 1 || n_tok <= 16) rows_shrink_block<1, TM, NW>(a, sh, e, p, rb, tok0, n_tok, lane, wave);
+  else rows_shrink_block<TM, TM, NW>(a, sh, e, p, rb, tok0, n_tok, lane, wave);
   return true;
 }
 
@@ -306,6 +323,7 @@ __global__ __launch_bounds__(kRowsThreads) void k_long_shrink(RowsArgs a, int n_
         load_x(s + 1);
         load_a(s + 1);
       }
+      rows_issue();
 #pragma unroll
       for (int tb = 0; tb < 4; ++tb) {
         const bf16x8 xf = *reinterpret_cast<const bf16x8*>(sh.x[buf] + (16 * tb + l16) * (2 * kLsK) +
@@ -386,14 +404,14 @@ __global__ __launch_bounds__(kRowsThreads) void k_rows(RowsArgs a) {
   constexpr int NP = GLU ? 2 : 1;
   constexpr int CPB = CB / NP;                   // column blocks
   union Shared {
-    RowsShrinkShared<1> shrink;
+    RowsShrinkShared<1, kRowsWaves> shrink;
     f32x4 red[kRowsWaves][CB][64];
     unsigned char x[kRowsXBytes];
   };
   __shared__ Shared sh;
-  const int tok0 = blockIdx.y * kRowsTokens, m = min(a.n - tok0, kRowsTokens);
+  const int m = a.n;   // at most 16
   if (static_cast<int>(blockIdx.x) < a.n_units) {
-    if (blockIdx.z == 0) (void)rows_shrink<1>(a, sh.shrink, blockIdx.x, NP, tok0, m);
+    if (blockIdx.z == 0) (void)rows_shrink<1, kRowsWaves>(a, sh.shrink, blockIdx.x, NP, 0, m);
     return;
   }
   // consecutive column blocks on one XCD, so that they share lines of the scales in its L2
@@ -449,9 +467,7 @@ __global__ __launch_bounds__(kRowsThreads) void k_rows(RowsArgs a) {
             const WView& w = a.w[proj(cb)];
             const int64_t o = g * w.ld_scale + col(cb) + 4 * lq;
             t.s[u][j][cb] = *reinterpret_cast<const u32x2*>(static_cast<const __bf16*>(w.scale) + o);
-            if (G < 128 && su * NS + j > g) t.s[u][j][cb] = u32x2{0u, 0u};   // past the last group
-            t.z[u][j][cb] = 0x08080808u;
-            if (WK == WKind::kInt4 && w.zero) t.z[u][j][cb] = *reinterpret_cast<const uint32_t*>(w.zero + o);
+            if constexpr (WK == WKind::kInt4) t.z[u][j][cb] = *reinterpret_cast<const uint32_t*>(rows_zeros(w) + o);
           }
         }
       }
@@ -501,7 +517,7 @@ __global__ __launch_bounds__(kRowsThreads) void k_rows(RowsArgs a) {
             const int j = f * NS / 4;
             const u32x2 s2 = t.s[u][j][cb];
             const f32x4 sc{bf16lo(s2.x), bf16hi(s2.x), bf16lo(s2.y), bf16hi(s2.y)};
-            const uint32_t zw = t.z[u][j][cb];
+            const uint32_t zw = WK == WKind::kInt4 && a.w[proj(cb)].zero ? t.z[u][j][cb] : 0x08080808u;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const float z = static_cast<float>((zw >> (8 * e)) & 0xFFu);
@@ -524,7 +540,7 @@ __global__ __launch_bounds__(kRowsThreads) void k_rows(RowsArgs a) {
       const int r = i / (len >> 3), k = 8 * (i - r * (len >> 3));
       u32x4 v{0u, 0u, 0u, 0u};
       if (k0 + k < a.h_in)
-        v = *reinterpret_cast<const u32x4*>(a.x + static_cast<int64_t>(tok0 + r) * a.ld_x + k0 + k);
+        v = *reinterpret_cast<const u32x4*>(a.x + static_cast<int64_t>(r) * a.ld_x + k0 + k);
       if constexpr (WK == WKind::kInt4) v = w4_xl_order(v);
       *reinterpret_cast<u32x4*>(sh.x + r * x_row + 2 * k) = v;
     }
@@ -557,137 +573,175 @@ __global__ __launch_bounds__(kRowsThreads) void k_rows(RowsArgs a) {
   if (a.part) {
     for (int it = threadIdx.x; it < CB * 64; it += kRowsThreads) {
       const int cb = it >> 6, l = it & 63, tok = l & 15;
-      if (tok < m) rows_put_part(a, NP, proj(cb), tok0 + tok, col(cb) + 4 * (l >> 4), total(cb, l));
+      if (tok < m) rows_put_part(a, NP, proj(cb), tok, col(cb) + 4 * (l >> 4), total(cb, l));
     }
   } else {
     for (int it = threadIdx.x; it < CPB * 64; it += kRowsThreads) {
       const int cp = it >> 6, l = it & 63, tok = l & 15;
       if (tok < m)
-        rows_put<GLU>(a, tok0 + tok, col0 + 16 * cp + 4 * (l >> 4), total(NP * cp, l), total(NP * cp + NP - 1, l));
+        rows_put<GLU>(a, tok, col0 + 16 * cp + 4 * (l >> 4), total(NP * cp, l), total(NP * cp + NP - 1, l));
     }
   }
 }
 
-// More tokens: 16 * TB of them and 8 waves of CB 16-row blocks each.  The
-// waves share x, 128 k at a time through two LDS buffers, so that its reads
-// from L2 (two bytes a token and k for every workgroup) stay below W's; each
-// wave reads its own rows of W straight into registers.  Both run D - 1 steps
-// ahead.  With GLU half of a wave's blocks are gate rows and half up rows.
+// More tokens: 16 * TB of them, 8 waves of two 16-row blocks of W^T each, and 4
+// waves that bring x.  The 8 share x, 128 k at a time through two LDS buffers,
+// so that its reads from L2 (two bytes a token and k for every workgroup) stay
+// below W's, and read their own rows of W straight into registers, D - 1 steps
+// ahead.  What bounds it is the issue of instructions, so the waves that bring
+// x also put it in the order the widening likes and form the sums of it that
+// the zero points multiply, and a fragment of x that was read from LDS meets
+// two blocks (one block to a wave: XX us against XX us for 33 tokens, 4-bit,
+// 4096 -> 2 x 12288).  With GLU a wave takes a gate block and the up block of
+// the same columns.
 //
 // x in LDS: rows of 256 bytes whose 16-byte chunks are XORed with the row, so
 // that the 16 rows of a fragment read cover all banks once.  The sums of x over
 // each group, which a zero point multiplies, are formed on the way in.
-template <WKind WK, int G, int TB, int CB, bool GLU>
-__global__ __launch_bounds__(kRowsThreads) void k_mid(RowsArgs a) {
+template <WKind WK, int G, int TB, bool GLU>
+__global__ __launch_bounds__(kMidThreads, 3) void k_mid(RowsArgs a) {
   constexpr int F = RowsLoad<WK>::kFrags, KS = 128;
   constexpr bool W4 = is_w4(WK), Z = WK == WKind::kInt4;
   constexpr int L = 4 / F;                       // loads of a row in one step
   constexpr int NS = W4 ? 128 / G : 1;           // scales of one step
-  constexpr int D = WK == WKind::kBf16 ? 2 : 3;  // steps in registers
+  constexpr int CB = 2;
+  // steps of W in registers
+  constexpr int D = W4 && G == 32 ? 2 : 3;
+  constexpr int DX = 4;                          // steps of x in a moving thread's registers
   constexpr int NP = GLU ? 2 : 1;
-  constexpr int XP = TB == 4 ? 2 : 1;            // 16-byte pieces of x a thread moves in one step
+  // With one group to a step, a 4-bit load's words meet the k that the lane
+  // itself holds; else they are exchanged so that each product covers 32
+  // consecutive k.
+  constexpr bool SWAP = W4 && G < 128;
   struct Stage {
     alignas(16) unsigned char x[16 * TB * 256];
     float xs[Z ? NS : 1][Z ? 16 * TB : 1];
   };
   union Shared {
-    RowsShrinkShared<TB> shrink;
+    RowsShrinkShared<TB, kMidThreads / 64> shrink;
     Stage st[2];
   };
   __shared__ Shared sh;
-  const int tok0 = blockIdx.y * 16 * TB, m = min(a.n - tok0, 16 * TB);
-  if (static_cast<int>(blockIdx.x) < a.n_units) {
-    if (blockIdx.z == 0) (void)rows_shrink<TB>(a, sh.shrink, blockIdx.x, NP, tok0, m);
+  // the grid's first a.n_units workgroups of each chunk shrink; then come the
+  // base's, an XCD's (every eighth) with all chunks of a column block side by
+  // side, so that its L2 holds the block's W for them
+  const int chunks = (a.n + 16 * TB - 1) / (16 * TB), per = (a.n_blocks + 7) >> 3;
+  int b = blockIdx.x - a.n_units * chunks;
+  if (b < 0) {
+    const int chunk = blockIdx.x / a.n_units, at = chunk * 16 * TB;
+    if (blockIdx.z == 0)
+      (void)rows_shrink<TB, kMidThreads / 64>(a, sh.shrink, blockIdx.x - chunk * a.n_units, NP, at, min(a.n - at, 16 * TB));
     return;
   }
-  const int b = blockIdx.x - a.n_units, per = (a.n_blocks + 7) >> 3;
-  const int blk = (b & 7) * per + (b >> 3);
+  const int xcd = b & 7;
+  b >>= 3;
+  const int blk = xcd * per + b / chunks, tok0 = (b % chunks) * 16 * TB, m = min(a.n - tok0, 16 * TB);
   if (blk >= a.n_blocks) return;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int l16 = lane & 15, lq = lane >> 4;
-  const int col0 = (blk * kRowsWaves + wave) * (16 * CB / NP);   // may start past h_out: such a wave only moves x
-  auto proj = [](int cb) { return GLU ? cb & 1 : 0; };
-  auto col = [&](int cb) { return col0 + 16 * (GLU ? cb >> 1 : cb); };
-
-  const char* wp[CB];
+  // the wave's output columns; may start past h_out: such a wave computes and does not store
+  const int col0 = (blk * kMidWaves + wave) * (16 * CB / NP);
+  auto proj = [](int cb) { return GLU ? cb : 0; };
+  auto col = [&](int cb) { return GLU ? col0 : col0 + 16 * cb; };
+  const char* wp[CB];   // uniform; lanes add 32-bit offsets
 #pragma unroll
   for (int cb = 0; cb < CB; ++cb)
-    wp[cb] = static_cast<const char*>(a.w[proj(cb)].w) + static_cast<int64_t>(min(col(cb), a.h_out - 16) + l16) * a.ld_w;
+    wp[cb] = static_cast<const char*>(a.w[proj(cb)].w) + min(col(cb), a.h_out - 16) * a.ld_w;
+  const uint32_t w_lane = static_cast<uint32_t>(l16 * a.ld_w) + 16 * lq;
   W4Table tab[NP];
   if constexpr (WK == WKind::kTable4) {
 #pragma unroll
     for (int p = 0; p < NP; ++p) tab[p].load(a.w[p].table);
   }
   const int steps = (a.h_in + KS - 1) / KS, parts = gridDim.z;
-  const int s0 = steps * blockIdx.z / parts, s1 = steps * (blockIdx.z + 1) / parts;
-  // a row's last load may reach past its end (h_in an odd multiple of 64): it
-  // is moved back into the row and x is zero there
+  const int s0 = steps * blockIdx.z / parts, n_steps = steps * (blockIdx.z + 1) / parts - s0;
+  // The column blocks start at different steps and wrap around: rows are a
+  // power of two apart as a rule, so workgroups that walked h_in in step would
+  // all read the same few memory channels at a time.
+  const int turn = blk % max(n_steps, 1);
+  auto step_at = [&](int i) {
+    i = min(i, n_steps - 1) + turn;
+    return s0 + (i < n_steps ? i : i - n_steps);
+  };
   const int row_bytes = W4 ? a.h_in / 2 : WK == WKind::kFp8 ? a.h_in : 2 * a.h_in;
 
-  // piece q of this thread: row xrow, chunk xchunk of the step's x
-  const __bf16* xsrc[XP];
-  int xdst[XP];
-  const int xchunk = tid & 15;
-#pragma unroll
-  for (int q = 0; q < XP; ++q) {
-    const int r = ((tid >> 4) + 32 * q) % (16 * TB);
-    xsrc[q] = a.x + static_cast<int64_t>(tok0 + min(r, m - 1)) * a.ld_x;
-    xdst[q] = r * 256 + ((xchunk ^ (r & 15)) << 4);
-  }
   struct Step {
     u32x4 w[L][CB];
-    u32x4 x[XP];
     u32x2 s[NS][W4 ? CB : 1];
     uint32_t z[NS][Z ? CB : 1];
   };
   auto load_w = [&](Step& t, int s) {
-    s = min(s, s1 - 1);
 #pragma unroll
-    for (int l = 0; l < L; ++l)
+    for (int l = 0; l < L; ++l) {
+      // a row's last load may reach past its end (h_in an odd multiple of 64): it
+      // is moved back into the row, and x is zero there
+      const int at = s * (64 * L) + 64 * l, over = max(at + 16 * lq + 16 - row_bytes, 0);
+      const uint32_t off = w_lane + static_cast<uint32_t>(at - over);   // the row's start or later: no wrap
 #pragma unroll
-      for (int cb = 0; cb < CB; ++cb)
-        t.w[l][cb] = ld16<true>(
-            reinterpret_cast<const u32x4*>(wp[cb] + min(s * (64 * L) + 64 * l + 16 * lq, row_bytes - 16)));
+      for (int cb = 0; cb < CB; ++cb) t.w[l][cb] = ld16<true>(reinterpret_cast<const u32x4*>(wp[cb] + off));
+    }
     if constexpr (W4) {
 #pragma unroll
       for (int j = 0; j < NS; ++j) {
         const int g = min(s * NS + j, a.h_in / G - 1);
 #pragma unroll
         for (int cb = 0; cb < CB; ++cb) {
-          const WView& w = a.w[proj(cb)];
-          const int64_t o = g * w.ld_scale + min(col(cb), a.h_out - 16) + 4 * lq;
-          t.s[j][cb] = *reinterpret_cast<const u32x2*>(static_cast<const __bf16*>(w.scale) + o);
-          if (G < 128 && s * NS + j > g) t.s[j][cb] = u32x2{0u, 0u};   // past the last group
-          if constexpr (Z) {
-            t.z[j][cb] = 0x08080808u;
-            if (w.zero) t.z[j][cb] = *reinterpret_cast<const uint32_t*>(w.zero + o);
-          }
+          const WView& wv = a.w[proj(cb)];
+          const int64_t o = g * wv.ld_scale + min(col(cb), a.h_out - 16);   // uniform
+          t.s[j][cb] = *reinterpret_cast<const u32x2*>(static_cast<const __bf16*>(wv.scale) + o + 4 * lq);
+          if constexpr (Z) t.z[j][cb] = *reinterpret_cast<const uint32_t*>(rows_zeros(wv) + o + 4 * lq);
         }
       }
     }
   };
-  auto load_x = [&](Step& t, int s) {
-    const int k = min(s, s1 - 1) * KS + 8 * xchunk;
+  if (wave >= kMidWaves) {
+    // ---- x: thread mt of the moving waves takes chunk mt % 16 of rows mt / 16, + RP, ...
+    constexpr int RP = 4 * kMidMovers, XP = 16 * TB / RP;
+    const int mt = tid - 64 * kMidWaves, xchunk = mt & 15, xrow = mt >> 4;
+    const __bf16* xsrc[XP];
 #pragma unroll
-    for (int q = 0; q < XP; ++q) t.x[q] = *reinterpret_cast<const u32x4*>(xsrc[q] + (k < a.h_in ? k : 0));
-  };
-  auto store_x = [&](const Step& t, int s, Stage& st) {
+    for (int q = 0; q < XP; ++q)
+      xsrc[q] = a.x + static_cast<int64_t>(tok0 + min(xrow + RP * q, m - 1)) * a.ld_x + 8 * xchunk;
+    u32x4 xr[DX][XP];
+    auto load_x = [&](u32x4 (&r)[XP], int s) {
+      const int k = s * KS + 8 * xchunk < a.h_in ? s * KS : 0;
 #pragma unroll
-    for (int q = 0; q < XP; ++q) {
-      u32x4 v = t.x[q];
-      if (s * KS + 8 * xchunk >= a.h_in) v = u32x4{0u, 0u, 0u, 0u};
-      *reinterpret_cast<u32x4*>(st.x + xdst[q]) = v;   // threads past a small tile write what others do
-      if constexpr (Z) {
-        float f = ((bf16lo(v.x) + bf16hi(v.x)) + (bf16lo(v.y) + bf16hi(v.y))) +
-                  ((bf16lo(v.z) + bf16hi(v.z)) + (bf16lo(v.w) + bf16hi(v.w)));
-        f += xor_lane<1>(f);
-        f += xor_lane<2>(f);
-        if constexpr (G >= 64) f += xor_lane<4>(f);
-        if constexpr (G >= 128) f += xor_lane<8>(f);
-        if ((xchunk & (G / 8 - 1)) == 0) st.xs[xchunk / (G / 8)][xdst[q] >> 8] = f;
+      for (int q = 0; q < XP; ++q) r[q] = *reinterpret_cast<const u32x4*>(xsrc[q] + k);
+    };
+    auto store_x = [&](const u32x4 (&r)[XP], int s, Stage& st) {
+      const bool in = s * KS + 8 * xchunk < a.h_in;   // past h_in (the last step's second half): zero
+#pragma unroll
+      for (int q = 0; q < XP; ++q) {
+        u32x4 v = r[q];
+        if (!in) v = u32x4{0u, 0u, 0u, 0u};
+        *reinterpret_cast<u32x4*>(st.x + (xrow + RP * q) * 256 + ((xchunk ^ ((xrow + RP * q) & 15)) << 4)) = Z ? w4_xl_order(v) : v;
+        if constexpr (Z) {
+          float f = ((bf16lo(v.x) + bf16hi(v.x)) + (bf16lo(v.y) + bf16hi(v.y))) +
+                    ((bf16lo(v.z) + bf16hi(v.z)) + (bf16lo(v.w) + bf16hi(v.w)));
+          f += xor_lane<1>(f);
+          f += xor_lane<2>(f);
+          if constexpr (G >= 64) f += xor_lane<4>(f);
+          if constexpr (G >= 128) f += xor_lane<8>(f);
+          if ((xchunk & (G / 8 - 1)) == 0) st.xs[xchunk / (G / 8)][xrow + RP * q] = f;
+        }
+      }
+    };
+#pragma unroll
+    for (int d = 0; d < DX; ++d) load_x(xr[d], step_at(d));
+    rows_issue();
+    store_x(xr[0], step_at(0), sh.st[0]);
+    for (int s = 0; s < n_steps; s += DX) {   // DX is even: buffers and ring slots come round together
+#pragma unroll
+      for (int i = 0; i < DX; ++i) {
+        if (s + i >= n_steps) break;
+        __syncthreads();   // x of step s + i is there; the other buffer's readers are done
+        load_x(xr[i % DX], step_at(s + i + DX));
+        rows_issue();
+        store_x(xr[(i + 1) % DX], step_at(s + i + 1), sh.st[(i + 1) & 1]);   // past the end: not read
       }
     }
-  };
+    return;
+  }
 
   f32x4 acc[CB][TB];
 #pragma unroll
@@ -697,7 +751,8 @@ __global__ __launch_bounds__(kRowsThreads) void k_mid(RowsArgs a) {
   const f32x4 none{0.f, 0.f, 0.f, 0.f};
 
   auto compute = [&](const Step& t, const Stage& st) {
-    auto x_at = [&](int tb, int chunk) {
+    auto x_at = [&](int tb, int f) {
+      const int chunk = F == 2 ? 8 * (f >> 1) + 2 * lq + (f & 1) : W4 && !SWAP ? 4 * lq + f : 4 * f + lq;
       return *reinterpret_cast<const bf16x8*>(st.x + (16 * tb + l16) * 256 + ((chunk ^ l16) << 4));
     };
     if constexpr (!W4) {
@@ -709,7 +764,7 @@ __global__ __launch_bounds__(kRowsThreads) void k_mid(RowsArgs a) {
           wf[cb] = WK == WKind::kBf16 ? __builtin_bit_cast(bf16x8, t.w[f / F][cb]) : rows_fp8(t.w[f / F][cb], f % F);
 #pragma unroll
         for (int tb = 0; tb < TB; ++tb) {
-          const bf16x8 xf = x_at(tb, WK == WKind::kBf16 ? 4 * f + lq : 8 * (f >> 1) + 2 * lq + (f & 1));
+          const bf16x8 xf = x_at(tb, f);
 #pragma unroll
           for (int cb = 0; cb < CB; ++cb) acc[cb][tb] = rows_mfma(wf[cb], xf, acc[cb][tb]);
         }
@@ -717,16 +772,16 @@ __global__ __launch_bounds__(kRowsThreads) void k_mid(RowsArgs a) {
     } else {
       u32x4 v[CB];
 #pragma unroll
-      for (int cb = 0; cb < CB; ++cb) v[cb] = rows_transpose4(t.w[0][cb]);
+      for (int cb = 0; cb < CB; ++cb) v[cb] = SWAP ? rows_transpose4(t.w[0][cb]) : t.w[0][cb];
       f32x4 sum[CB][TB];
 #pragma unroll
       for (int f = 0; f < 4; ++f) {
         bf16x8 wf[CB];
 #pragma unroll
-        for (int cb = 0; cb < CB; ++cb) wf[cb] = w4_widen<WK>(v[cb][f], tab[proj(cb)]);
+        for (int cb = 0; cb < CB; ++cb) wf[cb] = w4_widen<WK, true>(v[cb][f], tab[proj(cb)]);
 #pragma unroll
         for (int tb = 0; tb < TB; ++tb) {
-          const bf16x8 xf = x_at(tb, 4 * f + lq);
+          const bf16x8 xf = x_at(tb, f);
 #pragma unroll
           for (int cb = 0; cb < CB; ++cb)
             sum[cb][tb] = rows_mfma(wf[cb], xf, f % (4 / NS) == 0 ? none : sum[cb][tb]);
@@ -734,43 +789,43 @@ __global__ __launch_bounds__(kRowsThreads) void k_mid(RowsArgs a) {
         if (f % (4 / NS) == 4 / NS - 1) {   // the group ends here: scale its sum
           const int j = f * NS / 4;
 #pragma unroll
-          for (int tb = 0; tb < TB; ++tb) {
-            const float xs = Z ? st.xs[j][16 * tb + l16] : 0.f;
+          for (int cb = 0; cb < CB; ++cb) {
+            const u32x2 s2 = t.s[j][cb];
+            const f32x4 sc{bf16lo(s2.x), bf16hi(s2.x), bf16lo(s2.y), bf16hi(s2.y)};
+            f32x4 nz = none;
+            if constexpr (Z) {
+              const uint32_t zw = a.w[proj(cb)].zero ? t.z[j][cb] : 0x08080808u;
 #pragma unroll
-            for (int cb = 0; cb < CB; ++cb) {
-              const u32x2 s2 = t.s[j][cb];
-              const f32x4 sc{bf16lo(s2.x), bf16hi(s2.x), bf16lo(s2.y), bf16hi(s2.y)};
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                float g = sum[cb][tb][e];
-                if constexpr (Z) g = fmaf(-static_cast<float>((t.z[j][cb] >> (8 * e)) & 0xFFu), xs, g);
-                acc[cb][tb][e] = fmaf(sc[e], g, acc[cb][tb][e]);
-              }
+              for (int e = 0; e < 4; ++e) nz[e] = -static_cast<float>((zw >> (8 * e)) & 0xFFu);
             }
+#pragma unroll
+            for (int tb = 0; tb < TB; ++tb) {
+              const float xs = Z ? st.xs[j][16 * tb + l16] : 0.f;
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                acc[cb][tb][e] =
+                    fmaf(sc[e], Z ? fmaf(nz[e], xs, sum[cb][tb][e]) : sum[cb][tb][e], acc[cb][tb][e]);
+            }
+            // with four groups to a step, keeps their scales from being unpacked all at once
+            if (G == 32) __builtin_amdgcn_sched_barrier(0);
           }
         }
       }
     }
   };
 
-  // step s computes on ring slot s % D while its x is in LDS buffer s % 2; x
-  // of step s + 1 goes to the other buffer, whose readers passed the barrier
   Step ring[D];
 #pragma unroll
-  for (int d = 0; d < D - 1; ++d) {
-    load_x(ring[d], s0 + d);
-    load_w(ring[d], s0 + d);
-  }
-  store_x(ring[0], s0, sh.st[0]);
-  for (int s = s0; s < s1; s += 2 * D) {
+  for (int d = 0; d < D - 1; ++d) load_w(ring[d], step_at(d));
+  constexpr int TURN = D % 2 ? 2 * D : D;   // ring slots and LDS buffers both come round
+  for (int s = 0; s < n_steps; s += TURN) {
 #pragma unroll
-    for (int i = 0; i < 2 * D; ++i) {
-      if (s + i >= s1) break;
+    for (int i = 0; i < TURN; ++i) {
+      if (s + i >= n_steps) break;
       __syncthreads();
-      load_x(ring[(i + D - 1) % D], s + i + D - 1);
-      load_w(ring[(i + D - 1) % D], s + i + D - 1);
+      load_w(ring[(i + D - 1) % D], step_at(s + i + D - 1));
+      rows_issue();
       compute(ring[i % D], sh.st[i & 1]);
-      if (s + i + 1 < s1) store_x(ring[(i + 1) % D], s + i + 1, sh.st[(i + 1) & 1]);
     }
   }
 
@@ -784,69 +839,98 @@ __global__ __launch_bounds__(kRowsThreads) void k_mid(RowsArgs a) {
     }
 #pragma unroll
   for (int tb = 0; tb < TB; ++tb) {
-    const int tok = 16 * tb + l16;
-    if (tok >= m) continue;
+    if (16 * tb + l16 >= m) continue;
+    const int tok = tok0 + 16 * tb + l16;
 #pragma unroll
     for (int cb = 0; cb < CB; ++cb) {
       const int c = col(cb) + 4 * lq;
       if (c >= a.h_out) continue;
-      if (a.part) rows_put_part(a, NP, proj(cb), tok0 + tok, c, acc[cb][tb]);
-      else if (!GLU || proj(cb) == 0) rows_put<GLU>(a, tok0 + tok, c, acc[cb][tb], acc[cb + NP - 1][tb]);
+      if (a.part) rows_put_part(a, NP, proj(cb), tok, c, acc[cb][tb]);
+      else if (!GLU || cb == 0) rows_put<GLU>(a, tok, c, acc[cb][tb], acc[CB - 1][tb]);
     }
   }
 }
 
-// y = base sums + t B (and the gate), rounded once.  One thread per token and
-// 4 columns; a token's rank rows are read 8 at a time.
-constexpr int kFinishThreads = 128;
+// y = base sums + t B (and the gate), rounded once.  A workgroup takes one token
+// and kFinishCols columns; its four waves take every fourth rank row, 8 columns
+// to a lane, so that a rank of 64 is two rounds of 8 rows for each wave, and
+// their sums meet in LDS in wave order.  What bounds it is the chain of reads
+// (id, entry, page ids, B), so the page ids and t of all rank rows are read at
+// once and the projections' chains run side by side.
+constexpr int kFinishWaves = 4;
+constexpr int kFinishThreads = 64 * kFinishWaves;
+constexpr int kFinishCols = 64 * 8;
 template <bool GLU>
 __global__ __launch_bounds__(kFinishThreads) void k_rows_finish(RowsArgs a) {
   constexpr int NP = GLU ? 2 : 1;
-  const int tok = blockIdx.y;
-  const int c = 4 * (blockIdx.x * kFinishThreads + threadIdx.x);
-  if (c >= a.h_out) return;
+  __shared__ f32x4 red[kFinishWaves][NP][2][64];
+  const int tok = blockIdx.y, tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int c = blockIdx.x * kFinishCols + 8 * lane;
+  const bool in = c < a.h_out;   // h_out is a multiple of 64: all 8 columns or none
   const int id = a.ids ? a.ids[tok] : -1;
-  f32x4 v[NP];
+  f32x4 v[NP][2];
 #pragma unroll
-  for (int p = 0; p < NP; ++p)
-    v[p] = *reinterpret_cast<const f32x4*>(a.part + (static_cast<int64_t>(p) * a.n + tok) * a.h_out + c);
-  for (int z = 1; z < a.splits; ++z)
-#pragma unroll
-    for (int p = 0; p < NP; ++p)
-      v[p] += *reinterpret_cast<const f32x4*>(a.part + (static_cast<int64_t>(z * NP + p) * a.n + tok) * a.h_out + c);
-  if (id >= 0 && id < a.pv.n_slots) {
+  for (int p = 0; p < NP; ++p) {
+    v[p][0] = v[p][1] = f32x4{0.f, 0.f, 0.f, 0.f};
+    // the splits' sums: split z to wave z % kFinishWaves
+    for (int z = wave; in && z < a.splits; z += kFinishWaves) {
+      const f32x4* from = reinterpret_cast<const f32x4*>(
+          a.part + (static_cast<int64_t>(z * NP + p) * a.n + tok) * a.h_out + c);
+      v[p][0] += from[0];
+      v[p][1] += from[1];
+    }
+  }
+  if (in && id >= 0 && id < a.pv.n_slots) {
     const int h = static_cast<int>(a.pv.page_elems), ppr = a.h_out / h;
     const int cp = c / h, off = c - cp * h;
     const __bf16* pages = static_cast<const __bf16*>(a.pv.pages);
+    SlotEntry e[NP];
 #pragma unroll
-    for (int p = 0; p < NP; ++p) {
-      const SlotEntry e = a.pv.entries[static_cast<int64_t>(id) * a.pv.n_modules + a.module[p]];
-      const float* t = a.t + (static_cast<int64_t>(p) * a.n + tok) * kRowsTRow;
-      for (int j0 = 0; j0 < e.rank; j0 += 8) {
-        u32x2 b[8];
-        float tj[8];
+    for (int p = 0; p < NP; ++p) e[p] = a.pv.entries[static_cast<int64_t>(id) * a.pv.n_modules + a.module[p]];
+    const int most = max(e[0].rank, e[NP - 1].rank);
+    constexpr int R = 8;   // rank rows of one round of a wave
+    for (int j0 = wave; j0 < most; j0 += R * kFinishWaves) {
+      int32_t pid[NP][R];
+      float t[NP][R];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int jj = min(j0 + j, e.rank - 1);
-          const int pid = a.pv.page_ids[e.b_off + jj * ppr + cp];
-          b[j] = *reinterpret_cast<const u32x2*>(pages + static_cast<int64_t>(pid) * h + off);
-          tj[j] = t[jj];
+      for (int p = 0; p < NP; ++p)
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          const int j = j0 + r * kFinishWaves;
+          // rows past the rank read the zero page, whatever t is there counts as zero
+          pid[p][r] = j < e[p].rank ? a.pv.page_ids[e[p].b_off + j * ppr + cp] : a.pv.zero_page;
+          t[p][r] = j < e[p].rank ? a.t[(static_cast<int64_t>(p) * a.n + tok) * kRowsTRow + j] : 0.f;
         }
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (j0 + j < e.rank) {
-            v[p][0] = fmaf(tj[j], bf16lo(b[j].x), v[p][0]);
-            v[p][1] = fmaf(tj[j], bf16hi(b[j].x), v[p][1]);
-            v[p][2] = fmaf(tj[j], bf16lo(b[j].y), v[p][2]);
-            v[p][3] = fmaf(tj[j], bf16hi(b[j].y), v[p][3]);
+      for (int p = 0; p < NP; ++p) {
+        u32x4 b[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+          b[r] = *reinterpret_cast<const u32x4*>(pages + static_cast<int64_t>(pid[p][r]) * h + off);
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            v[p][q >> 1][2 * (q & 1)] = fmaf(t[p][r], bf16lo(b[r][q]), v[p][q >> 1][2 * (q & 1)]);
+            v[p][q >> 1][2 * (q & 1) + 1] = fmaf(t[p][r], bf16hi(b[r][q]), v[p][q >> 1][2 * (q & 1) + 1]);
           }
       }
     }
   }
-  __bf16 o[4];
 #pragma unroll
-  for (int e = 0; e < 4; ++e) o[e] = static_cast<__bf16>(GLU ? glu_act(a.act, v[0][e]) * v[NP - 1][e] : v[0][e]);
-  *reinterpret_cast<u32x2*>(a.y + static_cast<int64_t>(tok) * a.ld_y + c) = __builtin_bit_cast(u32x2, o);
+  for (int p = 0; p < NP; ++p)
+#pragma unroll
+    for (int q = 0; q < 2; ++q) red[wave][p][q][lane] = v[p][q];
+  __syncthreads();
+  if (wave >= 2 || !in) return;   // wave q writes columns 4 q .. + 4 of each lane's
+  f32x4 o[NP];
+#pragma unroll
+  for (int p = 0; p < NP; ++p) {
+    o[p] = red[0][p][wave][lane];
+#pragma unroll
+    for (int w = 1; w < kFinishWaves; ++w) o[p] += red[w][p][wave][lane];
+  }
+  rows_put<GLU>(a, tok, c + 4 * wave, o[0], o[NP - 1]);
 }
 
 }  // namespace lora
