@@ -12,9 +12,12 @@ using namespace lora;
 
 namespace {
 
-// Workspace that a call with ids needs at least (a shorter one only limits the split of h_in).
-size_t ws_need(bool rows, int n_proj, int32_t n_tokens, int64_t h_in, int64_t h_out) {
-  return rows ? rows_bytes(1, n_proj, n_tokens, h_out) : tiles_ws_bytes(n_proj, n_tokens, static_cast<int32_t>(h_in));
+// Workspace that a call with ids needs at least: the parts of a cut batch run one
+// after the other and share it.  (A shorter one than lora_fused_workspace_bytes
+// only limits the split of h_in.)
+size_t ws_need(const BatchCut& cut, int n_proj, int64_t h_in, int64_t h_out) {
+  return std::max(cut.rows > 0 ? rows_bytes(1, n_proj, cut.rows, h_out) : 0,
+                  cut.tiles > 0 ? tiles_ws_bytes(n_proj, cut.tiles, static_cast<int32_t>(h_in)) : 0);
 }
 
 bool aligned(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
@@ -67,9 +70,10 @@ lora_status base_call(const lora_pool* p, BaseCall& c, const int32_t* module, co
   if (ws_bytes > 0 && (!ws || !aligned(ws, 16))) return LORA_ERR_ARG;
   if (n_tokens == 0) return LORA_OK;
   const int64_t h_in = p->h_in[module[0]];
-  const bool rows = rows_faster(c.kind, c.group, n_proj, n_tokens, static_cast<int32_t>(h_in),
-                                static_cast<int32_t>(h_out));
-  if (ids && ws_bytes < ws_need(rows, n_proj, n_tokens, h_in, h_out)) return LORA_ERR_WORKSPACE;
+  const BatchCut cut = cut_batch(c.kind, c.group, n_proj, n_tokens, static_cast<int32_t>(h_in),
+                                 static_cast<int32_t>(h_out));
+  if (cut.tiles > 0 && !tiles_fit(c.glu, cut.tiles, static_cast<int32_t>(h_out))) return LORA_ERR_SHAPE;
+  if (ids && ws_bytes < ws_need(cut, n_proj, h_in, h_out)) return LORA_ERR_WORKSPACE;
   DeviceGuard g(p->device);
   if (!g.ok) return LORA_ERR_HIP;
   c.pv = p->view();
@@ -86,12 +90,20 @@ lora_status base_call(const lora_pool* p, BaseCall& c, const int32_t* module, co
   c.ws = static_cast<float*>(ws);
   c.ws_bytes = ws_bytes;
   hipStream_t s = static_cast<hipStream_t>(stream);
-  if (rows) return launch_rows(c, s);
-  if (ids) {
-    const lora_status st = launch_shrink(c, tiles_splits(c.n, c.h_in), s);
-    if (st != LORA_OK) return st;
+  if (cut.tiles > 0) {
+    c.n = cut.tiles;
+    if (ids) {
+      const lora_status st = launch_shrink(c, tiles_splits(c.n, c.h_in), s);
+      if (st != LORA_OK) return st;
+    }
+    const lora_status st = launch_tiles(c, s);
+    if (st != LORA_OK || cut.rows == 0) return st;
+    c.x += cut.tiles * ld_x;
+    c.y += cut.tiles * ld_y;
+    if (ids) c.ids += cut.tiles;
   }
-  return launch_tiles(c, s);
+  c.n = cut.rows;
+  return launch_rows(c, s);
 }
 
 bool bad_act(lora_act act) { return act != LORA_ACT_SILU && act != LORA_ACT_GELU && act != LORA_ACT_GELU_TANH; }
@@ -105,10 +117,11 @@ size_t lora_fused_workspace_bytes(const lora_pool* p, int32_t module, int32_t n_
   const int32_t h_in = static_cast<int32_t>(p->h_in[module]), h_out = static_cast<int32_t>(p->h_out[module]);
   size_t most = 0;   // over the kinds of weights, as the call is not known
   for (const auto& [kind, group] : {std::pair{WKind::kBf16, 0}, std::pair{WKind::kFp8, 0}, std::pair{WKind::kInt4, 32},
-                                    std::pair{WKind::kInt4, 128}})
-    most = std::max(most, rows_faster(kind, group, n_proj, n_tokens, h_in, h_out)
-                              ? rows_ws_bytes(kind, group, n_proj, n_tokens, h_in, h_out)
-                              : tiles_ws_bytes(n_proj, n_tokens, h_in));
+                                    std::pair{WKind::kInt4, 128}}) {
+    const BatchCut cut = cut_batch(kind, group, n_proj, n_tokens, h_in, h_out);
+    if (cut.rows > 0) most = std::max(most, rows_ws_bytes(kind, group, n_proj, cut.rows, h_in, h_out));
+    if (cut.tiles > 0) most = std::max(most, tiles_ws_bytes(n_proj, cut.tiles, h_in));
+  }
   return most;
 }
 

@@ -31,8 +31,12 @@ inline size_t rows_bytes(int splits, int n_proj, int32_t n_tokens, int64_t h_out
 }
 // What a call uses when it is given as much as it can use.
 size_t rows_ws_bytes(WKind kind, int group, int n_proj, int32_t n_tokens, int32_t h_in, int32_t h_out);
-// Whether a call streams W's rows (rows_kernels.hpp) or takes tiles (fused_gemm.hpp).
-bool rows_faster(WKind kind, int group, int n_proj, int32_t n_tokens, int32_t h_in, int32_t h_out);
+// A batch's first `tiles` tokens take tiles (fused_gemm.hpp), the `rows` after
+// them stream W's rows (rows_kernels.hpp); either may be 0.
+struct BatchCut {
+  int32_t tiles, rows;
+};
+BatchCut cut_batch(WKind kind, int group, int n_proj, int32_t n_tokens, int32_t h_in, int32_t h_out);   // rows.hip
 
 // Workspace of the tiled kernels: t of every token from each split of h_in.
 // The splits fill the GPU once, with 64 tokens and at least 256 k to each
@@ -52,5 +56,6 @@ inline size_t tiles_ws_bytes(int n_proj, int32_t n_tokens, int32_t h_in) {
 lora_status launch_shrink(const BaseCall& c, int splits, hipStream_t s);  // rows.hip: t of every token into c.ws
 lora_status launch_rows(const BaseCall& c, hipStream_t s);    // rows.hip
 lora_status launch_tiles(const BaseCall& c, hipStream_t s);   // tiles.hip
+bool tiles_fit(bool glu, int32_t n_tokens, int32_t h_out);
 
 }  // namespace lora

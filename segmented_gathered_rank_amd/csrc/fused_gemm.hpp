@@ -211,7 +211,20 @@ __global__ __launch_bounds__(kFgThreads, 1) void k_fused_gemm(FusedArgs a) {
   const int per_xcd = gridDim.x >> 3;
   const int tile = (blockIdx.x & 7) * per_xcd + (blockIdx.x >> 3);
   if (tile >= a.n_tiles) return;
-  const int rt = tile / a.n_ct, ct = tile - rt * a.n_ct;
+  int rt, ct;
+  if constexpr (GLU) {
+    // two projections' columns to a row tile: taken four row tiles at a time, so
+    // that the tiles an XCD runs together read a quarter of the weights from the
+    // other caches (4096 tokens, 4096 -> 2 x 12288: 838 -> 790 us)
+    constexpr int kRows = 4;
+    const int r0 = tile / (kRows * a.n_ct) * kRows, rows = min(kRows, (a.n + kFgBM - 1) / kFgBM - r0);
+    const int in = tile - r0 * a.n_ct;
+    ct = in / rows;
+    rt = r0 + in - ct * rows;
+  } else {
+    rt = tile / a.n_ct;
+    ct = tile - rt * a.n_ct;
+  }
   const int row0 = rt * kFgBM, col0 = ct * TC;
   const int nk = a.h_in / kFgBK;
 

@@ -86,21 +86,36 @@ RowsArgs rows_args(const BaseCall& c) {
 
 }  // namespace
 
-// Which kernels are faster, from their measured costs in microseconds.  Rows: 10
+// The kernels' measured costs in microseconds.  Rows: 10
 // to start, 0.45 for each 10^6 weights and chunk of 64 tokens, 6 for each 10^6
 // base sums written and read.  Tiles: 35 to start (with the shrink) and 0.032 for each k of every
 // round of 256 tiles.  Measured, rows against tiles: 4096x4096 4-bit 67 / 154 at
 // 512 tokens, 118 / 157 at 1024; 4096 -> 2 x 12288 bf16 113 / 154 at 128, 206 /
 // 128 at 256; 768 -> 2 x 2304 4-bit 45 / 60 at 512, 83 / 62 at 1024; 2048 ->
-// 2 x 8192 fp8, ranks up to 64, 83 / 143 at 256, 154 / 144 at 512.
-bool rows_faster(WKind kind, int group, int n_proj, int32_t n, int32_t h_in, int32_t h_out) {
-  if (n <= 64) return true;
+// 2 x 8192 fp8, ranks up to 64, 83 / 143 at 256, 154 / 144 at 512.  A few tokens
+// past a multiple of 256 may add a round of tiles for a batch's rest that rows
+// take in less: 2111 tokens, 4096 -> 2 x 8192 fp8: 450 us as tiles, XX as 2048 + 63.
+double rows_cost(WKind kind, int group, int n_proj, int32_t n, int32_t h_in, int32_t h_out) {
   const double cols = static_cast<double>(n_proj) * h_out;
-  const double rows = 10.0 + 0.45e-6 * cols * h_in * ((n + 63) / 64) * (is_w4(kind) && group == 32 ? 1.5 : 1.0) +
-                      6e-6 * n * cols;
-  const double n_tiles = ((static_cast<double>(n) + 255) / 256) * ((cols + 255) / 256);
-  const double rounds = static_cast<double>(static_cast<int64_t>((n_tiles + 255) / 256));
-  return rows < 35.0 + 0.032 * h_in * rounds;
+  return 10.0 + 0.45e-6 * cols * h_in * ((n + 63) / 64) * (is_w4(kind) && group == 32 ? 1.5 : 1.0) + 6e-6 * n * cols;
+}
+double tiles_cost(int n_proj, int32_t n, int32_t h_in, int32_t h_out) {
+  const int64_t cols = static_cast<int64_t>(n_proj) * h_out;
+  const int64_t n_tiles = (static_cast<int64_t>(n) + 255) / 256 * ((cols + 255) / 256);
+  return 35.0 + 0.032 * h_in * static_cast<double>((n_tiles + 255) / 256);
+}
+
+// Longest batch of the row-streaming kernels: the finish has a grid row for each token.
+constexpr int32_t kRowsMaxTokens = 32768;
+
+BatchCut cut_batch(WKind kind, int group, int n_proj, int32_t n, int32_t h_in, int32_t h_out) {
+  if (n <= kRowsTokens) return {0, n};
+  const double rows = rows_cost(kind, group, n_proj, n, h_in, h_out), tiles = tiles_cost(n_proj, n, h_in, h_out);
+  const int32_t tail = n % 256, whole = n - tail;
+  if (tail > 0 && whole > 0 &&
+      tiles_cost(n_proj, whole, h_in, h_out) + rows_cost(kind, group, n_proj, tail, h_in, h_out) < std::min(rows, tiles))
+    return {whole, tail};
+  return rows < tiles && n <= kRowsMaxTokens ? BatchCut{0, n} : BatchCut{n, 0};
 }
 
 size_t rows_ws_bytes(WKind kind, int group, int n_proj, int32_t n, int32_t h_in, int32_t h_out) {

@@ -19,7 +19,15 @@ void by_group(const FusedArgs& a, int32_t group, hipStream_t s) {
   else launch<WK, GLU, false>(a, s);
 }
 
+int64_t n_tiles(bool glu, int32_t n, int32_t h_out) {
+  const int tc = glu ? kFgGluCols : kFgBN;
+  return (static_cast<int64_t>(n) + kFgBM - 1) / kFgBM * ((h_out + tc - 1) / tc);
+}
+
 }  // namespace
+
+// 512 threads to a tile: within a launch's 2^32 - 1.
+bool tiles_fit(bool glu, int32_t n, int32_t h_out) { return n_tiles(glu, n, h_out) <= (int64_t(1) << 22); }
 
 lora_status launch_tiles(const BaseCall& c, hipStream_t s) {
   FusedArgs a{};
@@ -43,9 +51,7 @@ lora_status launch_tiles(const BaseCall& c, hipStream_t s) {
   a.group_shift = c.group == 128 ? 2 : c.group == 64 ? 1 : 0;
   const int tc = c.glu ? kFgGluCols : kFgBN;
   a.n_ct = (c.h_out + tc - 1) / tc;
-  const int64_t tiles = (static_cast<int64_t>(c.n) + kFgBM - 1) / kFgBM * a.n_ct;
-  if (tiles > (int64_t(1) << 22)) return LORA_ERR_SHAPE;   // 512 threads each: within a launch's 2^32 - 1
-  a.n_tiles = static_cast<int32_t>(tiles);
+  a.n_tiles = static_cast<int32_t>(n_tiles(c.glu, c.n, c.h_out));
   if (c.glu) {
     switch (c.kind) {
       case WKind::kBf16: launch<WKind::kBf16, true, false>(a, s); break;

@@ -21,8 +21,9 @@ class Problem:
     units of 16 bytes) and the scales (in units of 4)."""
 
     def __init__(self, op, kind, n, h_in, h_out, page=64, group=64, ranks=(16,), act="silu", ids="random", pads=0,
-                 seed=0, load=None, x=None):
+                 seed=0, load=None, x=None, w_scale=0.05):
         rng = np.random.default_rng(seed)
+        self.w_scale = w_scale
         self.op, self.kind, self.n, self.h_in, self.h_out, self.group, self.act = op, kind, n, h_in, h_out, group, act
         self.np = 2 if op == "glu" else 1
         self.ld_x, self.ld_y = h_in + 8 * pads, h_out + 4 * pads
@@ -64,7 +65,7 @@ class Problem:
         if kind == "bf16":
             self.ld_w = h_in + 8 * pads
             w = torch.full((h_out, self.ld_w), float("nan"), dtype=torch.bfloat16)
-            w[:, :h_in] = bf16(rng.normal(size=(h_out, h_in)) * 0.05)
+            w[:, :h_in] = bf16(rng.normal(size=(h_out, h_in)) * self.w_scale)
             self.wdev.append(w.cuda())
             self.w64.append(w[:, :h_in].double().numpy().T)
             self.wabs.append(np.abs(self.w64[-1]))

@@ -116,6 +116,56 @@ def test_non_finite_rows_stay_in_their_rows(op, kind, n, bad):
     p.close()
 
 
+def _rows_of(p, tokens):
+    """The problem's reference at some tokens only."""
+    x, ids = p.x64, p.ids64
+    p.x64, p.ids64 = x[tokens], ids[tokens]
+    v, bound = p.reference()
+    p.x64, p.ids64 = x, ids
+    return v, bound
+
+
+@pytest.mark.parametrize("op,kind,h_in,h_out,n", [("gemm", "int4", 1024, 1024, 64 * 256 + 40),
+                                                   ("gemm", "table", 1024, 1024, 64 * 256),
+                                                   ("glu", "fp8", 2048, 1024, 16 * 256 + 200),
+                                                   ("glu", "bf16", 512, 2048, 8 * 256 + 1)])
+def test_long_batches_and_their_rest(op, kind, h_in, h_out, n):
+    """Several rounds of tiles, and a rest past a multiple of 256 that goes another way; sampled
+    tokens around every seam, and nothing written behind the last."""
+    p = Problem(op, kind, n, h_in, h_out, page=256, group=128, ranks=(16, 33, 0, 7), ids="runs", seed=21, w_scale=0.02)
+    p.call()
+    torch.cuda.synchronize()
+    got = p.y.double().cpu().numpy()
+    assert np.all(got[n:] == SENTINEL)
+    rng = np.random.default_rng(1)
+    toks = np.unique(np.concatenate([np.arange(min(n, 300)), np.arange(n // 256 * 256 - 20, n),
+                                     rng.integers(0, n, 200)]))
+    v, bound = _rows_of(p, toks)
+    assert np.all(np.abs(got[toks] - v) <= bound)
+    p.close()
+
+
+@pytest.mark.parametrize("n", [40, 1000, 2100])
+@pytest.mark.parametrize("share", [0.0, 0.5])
+def test_smaller_workspaces(n, share):
+    """Without ids any workspace will do, none among them; with ids a shorter one than asked for
+    either limits the split of h_in or is refused, and never changes what is computed."""
+    p = Problem("gemm", "int4z", n, 2048, 256, page=256, group=64, ranks=(16, 5), seed=22)
+    nb = sgr.lora_fused_workspace_bytes(p.pool, 0, 1, n)
+    ws = torch.full((max(int(nb * share) // 16 * 4, 4),), float("nan"), device="cuda")
+    try:
+        p.call(ws=ws)
+        p.check()
+    except sgr.LoraError as e:
+        assert e.status == -9
+        torch.cuda.synchronize()
+        assert bool((p.y == SENTINEL).all())
+    ids, p.ids, p.ids64 = p.ids, None, None
+    sgr.lora_fused_gemm_w4(p.pool, 0, p.x, p.ld_x, p.wdev[0], None, n, p.y, p.ld_y, ws if share else None)
+    p.check()
+    p.close()
+
+
 @pytest.mark.parametrize("op,kind", [("gemm", "int4"), ("glu", "bf16"), ("glu", "fp8"), ("glu", "table")])
 def test_zero_tokens(op, kind):
     p = Problem(op, kind, 4, 128, 64, ranks=(8,))
