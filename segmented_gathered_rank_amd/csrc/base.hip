@@ -1,7 +1,6 @@
 // C ABI of the base products with 4-bit weights and of the gated feed-forward
 // product: argument checks and path selection.
 #include <algorithm>
-#include <utility>
 #include <cstdlib>
 
 #include "base_launch.hpp"
@@ -70,7 +69,7 @@ lora_status base_call(const lora_pool* p, BaseCall& c, const int32_t* module, co
   if (ws_bytes > 0 && (!ws || !aligned(ws, 16))) return LORA_ERR_ARG;
   if (n_tokens == 0) return LORA_OK;
   const int64_t h_in = p->h_in[module[0]];
-  const BatchCut cut = cut_batch(c.kind, c.group, n_proj, n_tokens, static_cast<int32_t>(h_in),
+  const BatchCut cut = cut_batch(n_proj, n_tokens, static_cast<int32_t>(h_in),
                                  static_cast<int32_t>(h_out));
   if (cut.tiles > 0 && !tiles_fit(c.glu, cut.tiles, static_cast<int32_t>(h_out))) return LORA_ERR_SHAPE;
   if (ids && ws_bytes < ws_need(cut, n_proj, h_in, h_out)) return LORA_ERR_WORKSPACE;
@@ -115,13 +114,11 @@ extern "C" {
 size_t lora_fused_workspace_bytes(const lora_pool* p, int32_t module, int32_t n_proj, int32_t n_tokens) {
   if (!p || module < 0 || module >= p->n_modules || n_proj < 1 || n_proj > 2 || n_tokens < 1) return 0;
   const int32_t h_in = static_cast<int32_t>(p->h_in[module]), h_out = static_cast<int32_t>(p->h_out[module]);
-  size_t most = 0;   // over the kinds of weights, as the call is not known
-  for (const auto& [kind, group] : {std::pair{WKind::kBf16, 0}, std::pair{WKind::kFp8, 0}, std::pair{WKind::kInt4, 32},
-                                    std::pair{WKind::kInt4, 128}}) {
-    const BatchCut cut = cut_batch(kind, group, n_proj, n_tokens, h_in, h_out);
-    if (cut.rows > 0) most = std::max(most, rows_ws_bytes(kind, group, n_proj, cut.rows, h_in, h_out));
-    if (cut.tiles > 0) most = std::max(most, tiles_ws_bytes(n_proj, cut.tiles, h_in));
-  }
+  const BatchCut cut = cut_batch(n_proj, n_tokens, h_in, h_out);
+  size_t most = cut.tiles > 0 ? tiles_ws_bytes(n_proj, cut.tiles, h_in) : 0;
+  if (cut.rows > 0)   // over the kinds of weights, as the call is not known
+    for (WKind kind : {WKind::kBf16, WKind::kFp8, WKind::kInt4})
+      most = std::max(most, rows_ws_bytes(kind, n_proj, cut.rows, h_in, h_out));
   return most;
 }
 

@@ -17,28 +17,40 @@ struct RowsPlan {
   int splits;    // of h_in over workgroups
 };
 
-// Base workgroups that a split of h_in aims at.
-constexpr int kRowsWgTarget = 256;
+// Workgroups that the GPU holds at a time: k_rows two to a CU, k_mid one.
+constexpr int kRowsResident = 512;
+constexpr int kMidResident = 256;
 
-RowsPlan rows_plan(WKind kind, int group, int n_proj, int32_t n, int32_t h_in, int32_t h_out, size_t ws_bytes) {
+RowsPlan rows_plan(WKind kind, int n_proj, int32_t n, int32_t h_in, int32_t h_out, size_t ws_bytes) {
   RowsPlan p{};
-  // with groups of 32 the scales of a step leave registers for 32 tokens only
-  // (64 tokens, 4160 -> 5440: 83 us with 64 at a time and spills, XX us with 32)
-  const int most = is_w4(kind) && group == 32 ? 2 : 4;
-  p.tb = n > 16 * most ? most : (n + 15) / 16;
+  p.tb = n > 48 ? 4 : (n + 15) / 16;
   p.chunks = (n + 16 * p.tb - 1) / (16 * p.tb);
-  auto split = [&](int cols, int steps, int min_steps) {
+  // the split of h_in with the least rounds of workgroups times steps of each,
+  // at `step` microseconds a step, 4 to start a workgroup, and the sums' way
+  // through the workspace
+  auto split = [&](int cols, int steps, int min_steps, int resident, double step) {
     p.blocks = (h_out * n_proj + cols - 1) / cols;
-    p.splits = std::max(1, std::min({kRowsMaxSplits, kRowsWgTarget / (p.blocks * p.chunks), steps / min_steps}));
-    while (p.splits > 1 && rows_bytes(p.splits, n_proj, n, h_out) > ws_bytes) --p.splits;
+    const double sums = 2e-6 * n * n_proj * h_out;
+    double best = 0.0;
+    p.splits = 0;
+    for (int s = 1; s <= kRowsMaxSplits && (s == 1 || s * min_steps <= steps); ++s) {
+      if (s > 1 && rows_bytes(s, n_proj, n, h_out) > ws_bytes) break;
+      const int64_t wgs = static_cast<int64_t>(p.blocks) * p.chunks * s;
+      const double cost = static_cast<double>((wgs + resident - 1) / resident) * ((steps + s - 1) / s * step + 4.0) +
+                          s * sums;
+      if (p.splits == 0 || cost < best) {
+        best = cost;
+        p.splits = s;
+      }
+    }
   };
   const int ks = is_w4(kind) ? 128 : kind == WKind::kFp8 ? 64 : 32, steps = (h_in + ks - 1) / ks;
   if (p.tb == 1) {
-    split(16 * kRowsCB, steps, kRowsWaves);
+    split(16 * kRowsCB, steps, kRowsWaves, kRowsResident, 1.0 / kRowsWaves);
     const int range = ((steps + p.splits - 1) / p.splits + 1) * ks;   // at most, of one workgroup
     p.x_lds = n * rows_x_stride(range) <= kRowsXBytes;
   }
-  if (!p.x_lds) split(32 * kMidWaves, (h_in + 127) / 128, 2);
+  if (!p.x_lds) split(32 * kMidWaves, (h_in + 127) / 128, 2, kMidResident, 1.5);
   return p;
 }
 
@@ -51,10 +63,8 @@ void by_tokens(const RowsArgs& base, const RowsPlan& p, hipStream_t s) {
   if (p.x_lds) hipLaunchKernelGGL((k_rows<WK, G, kRowsCB, GLU>), grid, wg, 0, s, a);
   else if (p.tb == 1) hipLaunchKernelGGL((k_mid<WK, G, 1, GLU>), grid, wg_mid, 0, s, a);
   else if (p.tb == 2) hipLaunchKernelGGL((k_mid<WK, G, 2, GLU>), grid, wg_mid, 0, s, a);
-  else if constexpr (G != 32) {
-    if (p.tb == 3) hipLaunchKernelGGL((k_mid<WK, G, 3, GLU>), grid, wg_mid, 0, s, a);
-    else hipLaunchKernelGGL((k_mid<WK, G, 4, GLU>), grid, wg_mid, 0, s, a);
-  }
+  else if (p.tb == 3) hipLaunchKernelGGL((k_mid<WK, G, 3, GLU>), grid, wg_mid, 0, s, a);
+  else hipLaunchKernelGGL((k_mid<WK, G, 4, GLU>), grid, wg_mid, 0, s, a);
 }
 
 template <WKind WK, bool GLU>
@@ -95,9 +105,9 @@ RowsArgs rows_args(const BaseCall& c) {
 // 2 x 8192 fp8, ranks up to 64, 83 / 143 at 256, 154 / 144 at 512.  A few tokens
 // past a multiple of 256 may add a round of tiles for a batch's rest that rows
 // take in less: 2111 tokens, 4096 -> 2 x 8192 fp8: 450 us as tiles, XX as 2048 + 63.
-double rows_cost(WKind kind, int group, int n_proj, int32_t n, int32_t h_in, int32_t h_out) {
+double rows_cost(int n_proj, int32_t n, int32_t h_in, int32_t h_out) {
   const double cols = static_cast<double>(n_proj) * h_out;
-  return 10.0 + 0.45e-6 * cols * h_in * ((n + 63) / 64) * (is_w4(kind) && group == 32 ? 1.5 : 1.0) + 6e-6 * n * cols;
+  return 10.0 + 0.45e-6 * cols * h_in * ((n + 63) / 64) + 6e-6 * n * cols;
 }
 double tiles_cost(int n_proj, int32_t n, int32_t h_in, int32_t h_out) {
   const int64_t cols = static_cast<int64_t>(n_proj) * h_out;
@@ -108,18 +118,18 @@ double tiles_cost(int n_proj, int32_t n, int32_t h_in, int32_t h_out) {
 // Longest batch of the row-streaming kernels: the finish has a grid row for each token.
 constexpr int32_t kRowsMaxTokens = 32768;
 
-BatchCut cut_batch(WKind kind, int group, int n_proj, int32_t n, int32_t h_in, int32_t h_out) {
+BatchCut cut_batch(int n_proj, int32_t n, int32_t h_in, int32_t h_out) {
   if (n <= kRowsTokens) return {0, n};
-  const double rows = rows_cost(kind, group, n_proj, n, h_in, h_out), tiles = tiles_cost(n_proj, n, h_in, h_out);
+  const double rows = rows_cost(n_proj, n, h_in, h_out), tiles = tiles_cost(n_proj, n, h_in, h_out);
   const int32_t tail = n % 256, whole = n - tail;
   if (tail > 0 && whole > 0 &&
-      tiles_cost(n_proj, whole, h_in, h_out) + rows_cost(kind, group, n_proj, tail, h_in, h_out) < std::min(rows, tiles))
+      tiles_cost(n_proj, whole, h_in, h_out) + rows_cost(n_proj, tail, h_in, h_out) < std::min(rows, tiles))
     return {whole, tail};
   return rows < tiles && n <= kRowsMaxTokens ? BatchCut{0, n} : BatchCut{n, 0};
 }
 
-size_t rows_ws_bytes(WKind kind, int group, int n_proj, int32_t n, int32_t h_in, int32_t h_out) {
-  return rows_bytes(rows_plan(kind, group, n_proj, n, h_in, h_out, SIZE_MAX).splits, n_proj, n, h_out);
+size_t rows_ws_bytes(WKind kind, int n_proj, int32_t n, int32_t h_in, int32_t h_out) {
+  return rows_bytes(rows_plan(kind, n_proj, n, h_in, h_out, SIZE_MAX).splits, n_proj, n, h_out);
 }
 
 lora_status launch_shrink(const BaseCall& c, int splits, hipStream_t s) {
@@ -133,7 +143,7 @@ lora_status launch_shrink(const BaseCall& c, int splits, hipStream_t s) {
 lora_status launch_rows(const BaseCall& c, hipStream_t s) {
   RowsArgs a = rows_args(c);
   const int n_proj = c.glu ? 2 : 1;
-  const RowsPlan p = rows_plan(c.kind, c.group, n_proj, c.n, c.h_in, c.h_out, c.ws_bytes);
+  const RowsPlan p = rows_plan(c.kind, n_proj, c.n, c.h_in, c.h_out, c.ws_bytes);
   a.splits = p.splits;
   if (c.ids || p.splits > 1) a.part = c.ws;
   if (c.ids) {

@@ -34,6 +34,7 @@ constexpr int kRowsWaves = 8;
 constexpr int kRowsThreads = 64 * kRowsWaves;
 constexpr int kMidWaves = 8;       // waves of k_mid that multiply
 constexpr int kMidMovers = 4;      // and that bring x
+constexpr int kMidCols = 32 * kMidWaves;   // rows of W^T of a workgroup
 constexpr int kMidThreads = 64 * (kMidWaves + kMidMovers);
 constexpr int kRowsTokens = 64;    // tokens of one workgroup; longer batches run as chunks of this many
 constexpr int kRowsMaxPpr = 32;    // A pages per rank row
@@ -588,9 +589,9 @@ __global__ __launch_bounds__(kRowsThreads) void k_rows(RowsArgs a) {
 // waves that bring x.  The 8 share x, 128 k at a time through two LDS buffers,
 // so that its reads from L2 (two bytes a token and k for every workgroup) stay
 // below W's, and read their own rows of W straight into registers, D - 1 steps
-// ahead.  What bounds it is the issue of instructions, so the waves that bring
-// x also put it in the order the widening likes and form the sums of it that
-// the zero points multiply, and a fragment of x that was read from LDS meets
+// ahead.  What bounds it is the issue of instructions and the registers, so the
+// waves that bring x also put it in the order the widening likes, form the sums
+// of it that the zero points multiply and bring the scales, and a fragment of x that was read from LDS meets
 // two blocks (one block to a wave: XX us against XX us for 33 tokens, 4-bit,
 // 4096 -> 2 x 12288).  With GLU a wave takes a gate block and the up block of
 // the same columns.
@@ -606,7 +607,7 @@ __global__ __launch_bounds__(kMidThreads, 3) void k_mid(RowsArgs a) {
   constexpr int NS = W4 ? 128 / G : 1;           // scales of one step
   constexpr int CB = 2;
   // steps of W in registers
-  constexpr int D = W4 && G == 32 ? 2 : 3;
+  constexpr int D = 3;
   constexpr int DX = 4;                          // steps of x in a moving thread's registers
   constexpr int NP = GLU ? 2 : 1;
   // With one group to a step, a 4-bit load's words meet the k that the lane
@@ -616,6 +617,8 @@ __global__ __launch_bounds__(kMidThreads, 3) void k_mid(RowsArgs a) {
   struct Stage {
     alignas(16) unsigned char x[16 * TB * 256];
     float xs[Z ? NS : 1][Z ? 16 * TB : 1];
+    u32x2 sc[W4 ? NS : 1][W4 ? kMidCols / 4 : 1];      // scales and zero points of the workgroup's W^T rows,
+    uint32_t zp[Z ? NS : 1][Z ? kMidCols / 4 : 1];     // 4 rows to an element
   };
   union Shared {
     RowsShrinkShared<TB, kMidThreads / 64> shrink;
@@ -667,8 +670,6 @@ __global__ __launch_bounds__(kMidThreads, 3) void k_mid(RowsArgs a) {
 
   struct Step {
     u32x4 w[L][CB];
-    u32x2 s[NS][W4 ? CB : 1];
-    uint32_t z[NS][Z ? CB : 1];
   };
   auto load_w = [&](Step& t, int s) {
 #pragma unroll
@@ -680,19 +681,6 @@ __global__ __launch_bounds__(kMidThreads, 3) void k_mid(RowsArgs a) {
 #pragma unroll
       for (int cb = 0; cb < CB; ++cb) t.w[l][cb] = ld16<true>(reinterpret_cast<const u32x4*>(wp[cb] + off));
     }
-    if constexpr (W4) {
-#pragma unroll
-      for (int j = 0; j < NS; ++j) {
-        const int g = min(s * NS + j, a.h_in / G - 1);
-#pragma unroll
-        for (int cb = 0; cb < CB; ++cb) {
-          const WView& wv = a.w[proj(cb)];
-          const int64_t o = g * wv.ld_scale + min(col(cb), a.h_out - 16);   // uniform
-          t.s[j][cb] = *reinterpret_cast<const u32x2*>(static_cast<const __bf16*>(wv.scale) + o + 4 * lq);
-          if constexpr (Z) t.z[j][cb] = *reinterpret_cast<const uint32_t*>(rows_zeros(wv) + o + 4 * lq);
-        }
-      }
-    }
   };
   if (wave >= kMidWaves) {
     // ---- x: thread mt of the moving waves takes chunk mt % 16 of rows mt / 16, + RP, ...
@@ -703,6 +691,24 @@ __global__ __launch_bounds__(kMidThreads, 3) void k_mid(RowsArgs a) {
     for (int q = 0; q < XP; ++q)
       xsrc[q] = a.x + static_cast<int64_t>(tok0 + min(xrow + RP * q, m - 1)) * a.ld_x + 8 * xchunk;
     u32x4 xr[DX][XP];
+    // and of the step's scales element mt % 64 of group mt / 64
+    const int sj = mt >> 6, sp = mt & 63;
+    const int sproj = GLU ? sp >> 5 : 0;
+    const int scol = min(GLU ? blk * (kMidCols / 2) + 4 * (sp & 31) : blk * kMidCols + 4 * sp, a.h_out - 4);
+    const WView& sw = a.w[sproj];
+    u32x2 sr[DX];
+    uint32_t zr[DX];
+    auto load_s = [&](int d, int s) {
+      if (!W4 || sj >= NS) return;   // whole waves
+      const int64_t o = static_cast<int64_t>(min(s * NS + sj, a.h_in / max(G, 1) - 1)) * sw.ld_scale + scol;
+      sr[d] = *reinterpret_cast<const u32x2*>(static_cast<const __bf16*>(sw.scale) + o);
+      if constexpr (Z) zr[d] = *reinterpret_cast<const uint32_t*>(rows_zeros(sw) + o);
+    };
+    auto store_s = [&](int d, Stage& st) {
+      if (!W4 || sj >= NS) return;
+      st.sc[sj][sp] = sr[d];
+      if constexpr (Z) st.zp[sj][sp] = sw.zero ? zr[d] : 0x08080808u;
+    };
     auto load_x = [&](u32x4 (&r)[XP], int s) {
       const int k = s * KS + 8 * xchunk < a.h_in ? s * KS : 0;
 #pragma unroll
@@ -727,17 +733,23 @@ __global__ __launch_bounds__(kMidThreads, 3) void k_mid(RowsArgs a) {
       }
     };
 #pragma unroll
-    for (int d = 0; d < DX; ++d) load_x(xr[d], step_at(d));
+    for (int d = 0; d < DX; ++d) {
+      load_x(xr[d], step_at(d));
+      load_s(d, step_at(d));
+    }
     rows_issue();
     store_x(xr[0], step_at(0), sh.st[0]);
+    store_s(0, sh.st[0]);
     for (int s = 0; s < n_steps; s += DX) {   // DX is even: buffers and ring slots come round together
 #pragma unroll
       for (int i = 0; i < DX; ++i) {
         if (s + i >= n_steps) break;
         __syncthreads();   // x of step s + i is there; the other buffer's readers are done
         load_x(xr[i % DX], step_at(s + i + DX));
+        load_s(i % DX, step_at(s + i + DX));
         rows_issue();
         store_x(xr[(i + 1) % DX], step_at(s + i + 1), sh.st[(i + 1) & 1]);   // past the end: not read
+        store_s((i + 1) % DX, sh.st[(i + 1) & 1]);
       }
     }
     return;
@@ -790,11 +802,12 @@ __global__ __launch_bounds__(kMidThreads, 3) void k_mid(RowsArgs a) {
           const int j = f * NS / 4;
 #pragma unroll
           for (int cb = 0; cb < CB; ++cb) {
-            const u32x2 s2 = t.s[j][cb];
+            const int piece = GLU ? cb * (kMidCols / 8) + 4 * wave + lq : 8 * wave + 4 * cb + lq;
+            const u32x2 s2 = st.sc[j][piece];
             const f32x4 sc{bf16lo(s2.x), bf16hi(s2.x), bf16lo(s2.y), bf16hi(s2.y)};
             f32x4 nz = none;
             if constexpr (Z) {
-              const uint32_t zw = a.w[proj(cb)].zero ? t.z[j][cb] : 0x08080808u;
+              const uint32_t zw = st.zp[j][piece];
 #pragma unroll
               for (int e = 0; e < 4; ++e) nz[e] = -static_cast<float>((zw >> (8 * e)) & 0xFFu);
             }
@@ -806,8 +819,6 @@ __global__ __launch_bounds__(kMidThreads, 3) void k_mid(RowsArgs a) {
                 acc[cb][tb][e] =
                     fmaf(sc[e], Z ? fmaf(nz[e], xs, sum[cb][tb][e]) : sum[cb][tb][e], acc[cb][tb][e]);
             }
-            // with four groups to a step, keeps their scales from being unpacked all at once
-            if (G == 32) __builtin_amdgcn_sched_barrier(0);
           }
         }
       }
