@@ -9,6 +9,7 @@ zero point per group, "table" with a 16-entry codebook), the widths, the batch
 and its adapters.
 """
 import math
+import weakref
 
 import torch
 
@@ -120,7 +121,7 @@ class _Pool:
 
     def __init__(self, case, a, b, scales):
         import segmented_gathered_rank_amd as sgr
-        self.sgr, m, page = sgr, _projections(case), case["page"]
+        m, page = _projections(case), case["page"]
         ranks = _ranks(case)
         pages = sum(ranks) * (case["h_in"] + case["h_out"]) // page * m
         self.h = sgr.lora_pool_create(torch.cuda.current_device(), sgr.LORA_BF16, page, pages, case["slots"], m,
@@ -130,9 +131,7 @@ class _Pool:
                 sgr.lora_pool_load(self.h, s, p, r, a[p][s, :r].contiguous(), b[p][s, :r].contiguous(),
                                    float(scales[s]))
         torch.cuda.synchronize()
-
-    def __del__(self):
-        self.sgr.lora_pool_destroy(self.h)
+        weakref.finalize(self, sgr.lora_pool_destroy, self.h)   # also at exit, while the library is there
 
 
 def prepare(case, seed):
