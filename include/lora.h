@@ -422,11 +422,15 @@ lora_status lora_fused_gemm_fp8w(const lora_pool *p, int32_t module,
                                  const float *w_scale, const int32_t *ids, int32_t n_tokens,
                                  void *y, int64_t ld_y, void *stream);
 
-/* Workspace bytes (device, 16-byte aligned, no initialization needed) of one
- * call of the four entry points below: n_proj is 1 for lora_fused_gemm_w4 and
- * 2 for the gated ones, `module` one of the call's modules.  0 where the call
- * needs none (long batches, bad arguments); a call without ids needs none
- * either.  Calls that share a workspace must be ordered on one stream; two
+/* Workspace bytes (device, 16-byte aligned, no initialization needed) that one
+ * call of the four entry points below makes use of: n_proj is 1 for
+ * lora_fused_gemm_w4 and 2 for the gated ones, `module` one of the call's
+ * modules; 0 on bad arguments.  With ids a call needs a workspace; a smaller
+ * one may be accepted (a short batch then splits h_in over fewer workgroups and
+ * runs slower), else it returns LORA_ERR_WORKSPACE.  Without ids it runs with
+ * any or none.  The split fixes the order of the sums, so calls with workspaces
+ * of different sizes may differ in the last bits of fp32 before the one
+ * rounding.  Calls that share a workspace must be ordered on one stream; two
  * captured graphs that may run at the same time need one each. */
 size_t lora_fused_workspace_bytes(const lora_pool *p, int32_t module, int32_t n_proj, int32_t n_tokens);
 
@@ -459,14 +463,17 @@ typedef struct {
  * and the exact v; sums, scales and the adapter term are fp32 (on the tiled
  * path t is multiplied by B as two bf16 parts of 16 significand bits), and y
  * is rounded once.  A non-finite value in a row of x makes that row's outputs
- * non-finite.
- * Short batches (decode) stream the weights' rows once per 64 tokens and run
- * as one launch without ids, two with them, through `ws`
- * (lora_fused_workspace_bytes); long ones run on tiles of 256 tokens.
+ * non-finite and no other's.  y must not overlap x, the weights or ws.
+ * Short batches (decode) stream the weights' rows once per 64 tokens, in one
+ * launch, or two with ids or with h_in split, through `ws`
+ * (lora_fused_workspace_bytes); long ones run on tiles of 256 tokens, behind a
+ * launch that forms t with ids, and a last part of a tile may take the short
+ * batches' way.  All launches go to `stream`; nothing else is enqueued, so a
+ * call can be captured.
  * The pool must be bf16 and h_in / page_elems at most 32.
  * Errors: ARG (null pointer, bad module, n_tokens < 0, a leading dimension
- * below the width, misalignment, a group other than 32, 64, 128, both zero and
- * table), DTYPE (pool not bf16), SHAPE (h_in not a multiple of the group, a
+ * below the width, misalignment of a pointer or leading dimension, ws_bytes > 0
+ * without ws, a group other than 32, 64, 128, both zero and table), DTYPE (pool not bf16), SHAPE (h_in not a multiple of the group, a
  * leading dimension or batch past what the launch can address), WORKSPACE,
  * HIP; nothing is launched on an argument error. */
 lora_status lora_fused_gemm_w4(const lora_pool *p, int32_t module,

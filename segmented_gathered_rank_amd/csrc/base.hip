@@ -33,15 +33,15 @@ lora_status check_base(const lora_pool* p, const int32_t* module, int n_proj, co
   if (h_in / p->page_elems > kFgMaxPpr || p->n_slots > kFgMaxSlots) return LORA_ERR_SHAPE;
   if (!x || !y) return LORA_ERR_ARG;
   if (ld_x < h_in || ld_y < h_out) return LORA_ERR_ARG;
-  // a tile's 256 rows of x and W^T are addressed with 32-bit byte offsets
-  if (ld_x > (int64_t(1) << 22) || h_in > (int64_t(1) << 22) || h_out > (int64_t(1) << 27)) return LORA_ERR_SHAPE;
+  // a tile's 256 rows of x are addressed with 32-bit byte offsets (widths are 2^20 at most in any pool)
+  if (ld_x > (int64_t(1) << 22)) return LORA_ERR_SHAPE;
   if (!aligned(x, 16) || ld_x % 8 != 0 || !aligned(y, 8) || ld_y % 4 != 0) return LORA_ERR_ARG;
   return LORA_OK;
 }
 
 lora_status check_rows_of_w(const void* w, int64_t ld_bytes, int64_t row_bytes) {
   if (!w || !aligned(w, 16) || ld_bytes % 16 != 0 || ld_bytes < row_bytes) return LORA_ERR_ARG;
-  return ld_bytes > (int64_t(1) << 23) ? LORA_ERR_SHAPE : LORA_OK;
+  return ld_bytes > (int64_t(1) << 23) ? LORA_ERR_SHAPE : LORA_OK;   // a tile's 256 rows: 32-bit offsets
 }
 
 lora_status check_w4(const lora_pool* p, int32_t module, const lora_w4* w) {

@@ -20,7 +20,7 @@ struct BaseCall {
   int32_t module[2];
   int32_t act;
   size_t ws_bytes;
-  float* ws;              // with ids: rows_ws_bytes(...) or tiles_ws_bytes(...)
+  float* ws;              // may be null without ids; its size then bounds the split of h_in
 };
 
 // Workspace of the row-streaming kernels: the base sums of each split of h_in,

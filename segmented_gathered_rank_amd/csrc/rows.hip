@@ -27,7 +27,9 @@ RowsPlan rows_plan(WKind kind, int n_proj, int32_t n, int32_t h_in, int32_t h_ou
   p.chunks = (n + 16 * p.tb - 1) / (16 * p.tb);
   // the split of h_in with the least rounds of workgroups times steps of each,
   // at `step` microseconds a step, 4 to start a workgroup, and the sums' way
-  // through the workspace
+  // through the workspace (a call, split against unsplit: 64 tokens, 4096 ->
+  // 4096 4-bit 18 us in 8 splits against 61; 33 tokens, 4096 -> 2 x 12288 4-bit 40
+  // in 2 against 60; 64 tokens, 2048 -> 2 x 8192 fp8 46 in 4 against 52)
   auto split = [&](int cols, int steps, int min_steps, int resident, double step) {
     p.blocks = (h_out * n_proj + cols - 1) / cols;
     const double sums = 2e-6 * n * n_proj * h_out;
@@ -96,15 +98,16 @@ RowsArgs rows_args(const BaseCall& c) {
 
 }  // namespace
 
-// The kernels' measured costs in microseconds.  Rows: 10
-// to start, 0.45 for each 10^6 weights and chunk of 64 tokens, 6 for each 10^6
-// base sums written and read.  Tiles: 35 to start (with the shrink) and 0.032 for each k of every
-// round of 256 tiles.  Measured, rows against tiles: 4096x4096 4-bit 67 / 154 at
-// 512 tokens, 118 / 157 at 1024; 4096 -> 2 x 12288 bf16 113 / 154 at 128, 206 /
-// 128 at 256; 768 -> 2 x 2304 4-bit 45 / 60 at 512, 83 / 62 at 1024; 2048 ->
-// 2 x 8192 fp8, ranks up to 64, 83 / 143 at 256, 154 / 144 at 512.  A few tokens
-// past a multiple of 256 may add a round of tiles for a batch's rest that rows
-// take in less: 2111 tokens, 4096 -> 2 x 8192 fp8: 450 us as tiles, XX as 2048 + 63.
+// The kernels' measured costs in microseconds.  Rows: 10 to start, 0.45 for each
+// 10^6 weights and chunk of 64 tokens, 6 for each 10^6 base sums written and
+// read.  Tiles: 35 to start (with the shrink) and 0.032 for each k of every round
+// of 256 tiles.  Measured, rows against tiles: 4096x4096 4-bit 67 / 154 at 512
+// tokens, 118 / 157 at 1024; 4096 -> 2 x 12288 bf16 113 / 154 at 128, 206 / 128
+// at 256; 768 -> 2 x 2304 4-bit 45 / 60 at 512, 83 / 62 at 1024; 2048 -> 2 x 8192
+// fp8, ranks up to 64, 83 / 143 at 256, 154 / 144 at 512.  A few tokens past a
+// multiple of 256 may add a round of tiles for a batch's rest that rows take in
+// less: 4096 -> 2 x 8192 fp8, 2111 tokens as 2048 + 63 take 350 us, where 2304,
+// as many tiles as 2111 alone would be, take 410.
 double rows_cost(int n_proj, int32_t n, int32_t h_in, int32_t h_out) {
   const double cols = static_cast<double>(n_proj) * h_out;
   return 10.0 + 0.45e-6 * cols * h_in * ((n + 63) / 64) + 6e-6 * n * cols;

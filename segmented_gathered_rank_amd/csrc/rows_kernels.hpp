@@ -1,15 +1,16 @@
-// Base product for few tokens (decode): y^T = W^T x^T streamed once over W,
-// with the adapters' shrink in the same launch.
+// Base products for short batches (decode): y^T = W^T x^T with W streamed once
+// for every 64 tokens, and the adapters' shrink in the same launch.
 //
-// The weights are all there is to read (n_tokens flops pairs for each), so the
-// kernel is a stream of W^T rows: a workgroup takes 16 * CB rows (output
-// columns), its 8 waves split h_in between them, and each lane reads 16 bytes
-// of one row at a time.  The products run on v_mfma_f32_16x16x32_bf16 with a
-// W^T row block as the A operand and 16 tokens as the B operand: with few
-// tokens most of the matrix work is on repeated columns, but the matrix cores
+// The weights are nearly all there is to read (2 n_tokens flops for each), so
+// the kernels are streams of W^T rows (output columns), each lane reading 16
+// bytes of one row at a time.  The products run on v_mfma_f32_16x16x32_bf16 with
+// a 16-row block of W^T as the A operand and 16 tokens as the B operand: with
+// few tokens most of the matrix work is on repeated columns, but the matrix cores
 // are idle otherwise and the vector ALU is left to the widening of the codes.
-// The waves' sums meet in LDS, in wave order, so the result does not depend
-// on timing.
+// Up to 16 tokens whose x fits in LDS run on k_rows, whose waves split h_in;
+// more on k_mid, whose waves each take rows of their own and share x.  Where the
+// columns alone do not fill the GPU, workgroups split h_in too.  Waves' and
+// splits' sums are added in their order, so the result does not depend on timing.
 //
 // 4-bit codes.  A lane's 16 bytes are 32 codes of one row; an exchange of
 // words between the four lane groups (v_permlane32_swap, v_permlane16_swap: a
@@ -17,13 +18,14 @@
 // consecutive k each, so that every group of 32, 64 or 128 k is whole MFMAs.
 // Those run on the codes' exact integers (or the codebook's values), and the
 // group's sum is scaled once in fp32.  A zero point z enters as
-// s (sum q x - z sum x), with sum x from one more MFMA whose A operand is
-// all ones.
+// s (sum q x - z sum x), with the sum of x over the group formed beside it.
 //
 // Adapters.  t = s_a x A_a^T is the same kind of product with A's rank rows
-// as the weights; its workgroups come first in the grid, one for each
-// 16-row block of each distinct adapter of a chunk's tokens.  Base sums and t then go through the workspace to a second, small
-// kernel that adds t B, applies the gate and rounds once.
+// as the weights; its workgroups come first in the grid, one for each 16-row
+// block of each distinct adapter of a chunk's tokens.  Base sums and t then go
+// through the workspace to a second, small kernel (k_rows_finish) that adds t B,
+// applies the gate and rounds once.  A call without adapters writes y from the
+// first kernel unless h_in is split.
 #pragma once
 
 #include "base_args.hpp"
@@ -36,7 +38,7 @@ constexpr int kMidWaves = 8;       // waves of k_mid that multiply
 constexpr int kMidMovers = 4;      // and that bring x
 constexpr int kMidCols = 32 * kMidWaves;   // rows of W^T of a workgroup
 constexpr int kMidThreads = 64 * (kMidWaves + kMidMovers);
-constexpr int kRowsTokens = 64;    // tokens of one workgroup; longer batches run as chunks of this many
+constexpr int kRowsTokens = 64;    // tokens of one workgroup at most; longer batches run in chunks
 constexpr int kRowsMaxPpr = 32;    // A pages per rank row
 constexpr int kRowsTRow = kMaxRank;
 
@@ -396,6 +398,10 @@ __device__ __forceinline__ bf16x8 rows_fp8(u32x4 v, int h) {
 // h_in is split between gridDim.z workgroups and their waves, each of which
 // reads U loads of each of its rows one batch ahead of the products.  x waits
 // in LDS: loads return in order, so x loaded in between would hold up W.
+// Bound by the read of W: bf16, 1 token, 4096 -> 2 x 11264 37 us (5.0 TB/s);
+// 4-bit with zero points, 1 token, 8192 -> 28672 35 us (3.4 TB/s, where the
+// widening's and scaling's instructions are as long as the read); small layers
+// by the launch (4-bit, 768 -> 768 5.3 us).
 template <WKind WK, int G, int CB, bool GLU>
 __global__ __launch_bounds__(kRowsThreads) void k_rows(RowsArgs a) {
   constexpr int F = RowsLoad<WK>::kFrags, KS = RowsLoad<WK>::kK;
@@ -585,20 +591,24 @@ __global__ __launch_bounds__(kRowsThreads) void k_rows(RowsArgs a) {
   }
 }
 
-// More tokens: 16 * TB of them, 8 waves of two 16-row blocks of W^T each, and 4
-// waves that bring x.  The 8 share x, 128 k at a time through two LDS buffers,
-// so that its reads from L2 (two bytes a token and k for every workgroup) stay
-// below W's, and read their own rows of W straight into registers, D - 1 steps
-// ahead.  What bounds it is the issue of instructions and the registers, so the
-// waves that bring x also put it in the order the widening likes, form the sums
-// of it that the zero points multiply and bring the scales, and a fragment of x that was read from LDS meets
-// two blocks (one block to a wave: XX us against XX us for 33 tokens, 4-bit,
-// 4096 -> 2 x 12288).  With GLU a wave takes a gate block and the up block of
-// the same columns.
+// More tokens, or an x past LDS: 16 * TB tokens to a workgroup, 8 waves of two
+// 16-row blocks of W^T each, and 4 waves that bring x.  The 8 share x, 128 k at
+// a time through two LDS buffers, so that its reads from L2 (two bytes a token
+// and k for every workgroup) stay below W's, and read their own rows of W
+// straight into registers, D - 1 steps ahead.  Loads return in order, so waves
+// that waited for x would wait for all of W's steps too: that is why other waves
+// bring it.  What bounds the kernel is the issue of instructions and the
+// registers, so those waves also put x in the order the widening likes, form the
+// sums of it that the zero points multiply and bring the scales, and a fragment
+// of x that was read from LDS meets two blocks (33 tokens, 4-bit, 4096 ->
+// 2 x 12288: 30 to 31 us; one block to a wave 34 to 42, 4 or 16 waves and other
+// depths no better).  With GLU a wave takes a gate block and the up block of the
+// same columns.  Measured: that case with zero points and adapters 34 us
+// (1.5 TB/s of codes and scales); fp8, 64 tokens, 2048 -> 2 x 8192 with 64
+// adapters of ranks 8 to 64 32 us, 16 to 18 of them the weights'.
 //
 // x in LDS: rows of 256 bytes whose 16-byte chunks are XORed with the row, so
-// that the 16 rows of a fragment read cover all banks once.  The sums of x over
-// each group, which a zero point multiplies, are formed on the way in.
+// that the 16 rows of a fragment read cover all banks once.
 template <WKind WK, int G, int TB, bool GLU>
 __global__ __launch_bounds__(kMidThreads, 3) void k_mid(RowsArgs a) {
   constexpr int F = RowsLoad<WK>::kFrags, KS = 128;
@@ -606,8 +616,7 @@ __global__ __launch_bounds__(kMidThreads, 3) void k_mid(RowsArgs a) {
   constexpr int L = 4 / F;                       // loads of a row in one step
   constexpr int NS = W4 ? 128 / G : 1;           // scales of one step
   constexpr int CB = 2;
-  // steps of W in registers
-  constexpr int D = 3;
+  constexpr int D = 3;                           // steps of W in registers
   constexpr int DX = 4;                          // steps of x in a moving thread's registers
   constexpr int NP = GLU ? 2 : 1;
   // With one group to a step, a 4-bit load's words meet the k that the lane
@@ -720,7 +729,8 @@ __global__ __launch_bounds__(kMidThreads, 3) void k_mid(RowsArgs a) {
       for (int q = 0; q < XP; ++q) {
         u32x4 v = r[q];
         if (!in) v = u32x4{0u, 0u, 0u, 0u};
-        *reinterpret_cast<u32x4*>(st.x + (xrow + RP * q) * 256 + ((xchunk ^ ((xrow + RP * q) & 15)) << 4)) = Z ? w4_xl_order(v) : v;
+        *reinterpret_cast<u32x4*>(st.x + (xrow + RP * q) * 256 + ((xchunk ^ ((xrow + RP * q) & 15)) << 4)) =
+            Z ? w4_xl_order(v) : v;
         if constexpr (Z) {
           float f = ((bf16lo(v.x) + bf16hi(v.x)) + (bf16lo(v.y) + bf16hi(v.y))) +
                     ((bf16lo(v.z) + bf16hi(v.z)) + (bf16lo(v.w) + bf16hi(v.w)));
@@ -867,7 +877,9 @@ __global__ __launch_bounds__(kMidThreads, 3) void k_mid(RowsArgs a) {
 // to a lane, so that a rank of 64 is two rounds of 8 rows for each wave, and
 // their sums meet in LDS in wave order.  What bounds it is the chain of reads
 // (id, entry, page ids, B), so the page ids and t of all rank rows are read at
-// once and the projections' chains run side by side.
+// once and the projections' chains run side by side: 2.9 us for one token and
+// 768 columns, 4.3 for 64 tokens of rank 16 and 4096, 14 for 64 of ranks 8 to 64
+// and 2 x 8192.
 constexpr int kFinishWaves = 4;
 constexpr int kFinishThreads = 64 * kFinishWaves;
 constexpr int kFinishCols = 64 * 8;

@@ -166,6 +166,39 @@ def test_smaller_workspaces(n, share):
     p.close()
 
 
+def _least_workspace(p):
+    """Base sums of one split and t, fp32: with it h_in is not split over workgroups."""
+    return torch.full((p.np * p.n * (p.h_out + 64),), float("nan"), device="cuda")
+
+
+@pytest.mark.parametrize("op,kind,group", FORMS, ids=IDS)
+@pytest.mark.parametrize("n", [1, 9, 16])
+@pytest.mark.parametrize("ws", ["least", "asked for", "none"])
+def test_wide_rows_of_few_tokens(op, kind, group, n, ws):
+    """h_in past what LDS holds of x (the 64-token kernel with one block of 16), and the same split
+    into ranges that LDS does hold; h_in ends half way into the last 128 where the group allows."""
+    h_in, page = (4224, 384) if group == 128 else (4160, 320)
+    p = Problem(op, kind, n, h_in, 4 * page, group=group or 64, page=page, ranks=(16, 40, 0, 9), seed=31 + n,
+                ids="null" if ws == "none" else "random", w_scale=0.02)
+    if ws == "none":
+        p.ws = torch.empty(0, device="cuda")
+    p.call(ws=_least_workspace(p) if ws == "least" else None)
+    p.check(what=ws)
+    p.close()
+
+
+@pytest.mark.parametrize("op,kind,group", FORMS, ids=IDS)
+@pytest.mark.parametrize("n", [24, 48, 60])
+@pytest.mark.parametrize("ws", ["least", "asked for"])
+def test_wide_rows_of_more_tokens(op, kind, group, n, ws):
+    """Every count of 16-token blocks over more steps of h_in than are held at a time, whole and split."""
+    h_in, page = (2176, 128) if group == 128 else (2240, 320)
+    p = Problem(op, kind, n, h_in, 5 * page, group=group or 64, page=page, ranks=(16, 64, 0, 9), seed=41 + n, w_scale=0.02)
+    p.call(ws=_least_workspace(p) if ws == "least" else None)
+    p.check(what=ws)
+    p.close()
+
+
 @pytest.mark.parametrize("op,kind", [("gemm", "int4"), ("glu", "bf16"), ("glu", "fp8"), ("glu", "table")])
 def test_zero_tokens(op, kind):
     p = Problem(op, kind, 4, 128, 64, ranks=(8,))
