@@ -473,9 +473,10 @@ typedef struct {
  * The pool must be bf16 and h_in / page_elems at most 32.
  * Errors: ARG (null pointer, bad module, n_tokens < 0, a leading dimension
  * below the width, misalignment of a pointer or leading dimension, ws_bytes > 0
- * without ws, a group other than 32, 64, 128, both zero and table), DTYPE (pool not bf16), SHAPE (h_in not a multiple of the group, a
- * leading dimension or batch past what the launch can address), WORKSPACE,
- * HIP; nothing is launched on an argument error. */
+ * without ws, a group other than 32, 64, 128, both zero and table), DTYPE (pool
+ * not bf16), SHAPE (h_in not a multiple of the group, a leading dimension or
+ * batch past what the launch can address), WORKSPACE, HIP; nothing is launched
+ * on an argument error. */
 lora_status lora_fused_gemm_w4(const lora_pool *p, int32_t module,
                                const void *x, int64_t ld_x, const lora_w4 *w,
                                const int32_t *ids, int32_t n_tokens,

@@ -118,7 +118,7 @@ size_t lora_fused_workspace_bytes(const lora_pool* p, int32_t module, int32_t n_
   size_t most = cut.tiles > 0 ? tiles_ws_bytes(n_proj, cut.tiles, h_in) : 0;
   if (cut.rows > 0)   // over the kinds of weights, as the call is not known
     for (WKind kind : {WKind::kBf16, WKind::kFp8, WKind::kInt4})
-      most = std::max(most, rows_ws_bytes(kind, n_proj, cut.rows, h_in, h_out));
+      most = std::max(most, rows_ws_bytes(kind, n_proj, cut.rows, p->n_slots, h_in, h_out));
   return most;
 }
 

@@ -30,7 +30,7 @@ inline size_t rows_bytes(int splits, int n_proj, int32_t n_tokens, int64_t h_out
   return sizeof(float) * n_proj * static_cast<size_t>(n_tokens) * static_cast<size_t>(splits * h_out + kMaxRank);
 }
 // What a call uses when it is given as much as it can use.
-size_t rows_ws_bytes(WKind kind, int n_proj, int32_t n_tokens, int32_t h_in, int32_t h_out);
+size_t rows_ws_bytes(WKind kind, int n_proj, int32_t n_tokens, int32_t slots, int32_t h_in, int32_t h_out);
 // A batch's first `tiles` tokens take tiles (fused_gemm.hpp), the `rows` after
 // them stream W's rows (rows_kernels.hpp); either may be 0.
 struct BatchCut {

@@ -15,21 +15,24 @@ struct RowsPlan {
   int blocks;    // base workgroups of one split and chunk
   int chunks;    // of 16 * tb tokens
   int splits;    // of h_in over workgroups
+  int units;     // shrink workgroups of one chunk
 };
 
 // Workgroups that the GPU holds at a time: k_rows two to a CU, k_mid one.
 constexpr int kRowsResident = 512;
 constexpr int kMidResident = 256;
 
-RowsPlan rows_plan(WKind kind, int n_proj, int32_t n, int32_t h_in, int32_t h_out, size_t ws_bytes) {
+// adapters: how many different ones the batch may hold (0: a call without ids).
+RowsPlan rows_plan(WKind kind, int n_proj, int32_t n, int32_t adapters, int32_t h_in, int32_t h_out, size_t ws_bytes) {
   RowsPlan p{};
   p.tb = n > 48 ? 4 : (n + 15) / 16;
   p.chunks = (n + 16 * p.tb - 1) / (16 * p.tb);
+  p.units = (std::min({n, 16 * p.tb, adapters}) * n_proj + 7) / 8 * 8;
   // the split of h_in with the least rounds of workgroups times steps of each,
   // at `step` microseconds a step, 4 to start a workgroup, and the sums' way
   // through the workspace (a call, split against unsplit: 64 tokens, 4096 ->
   // 4096 4-bit 18 us in 8 splits against 61; 33 tokens, 4096 -> 2 x 12288 4-bit 40
-  // in 2 against 60; 64 tokens, 2048 -> 2 x 8192 fp8 46 in 4 against 52)
+  // in 2 against 60)
   auto split = [&](int cols, int steps, int min_steps, int resident, double step) {
     p.blocks = (h_out * n_proj + cols - 1) / cols;
     const double sums = 2e-6 * n * n_proj * h_out;
@@ -52,7 +55,11 @@ RowsPlan rows_plan(WKind kind, int n_proj, int32_t n, int32_t h_in, int32_t h_ou
     const int range = ((steps + p.splits - 1) / p.splits + 1) * ks;   // at most, of one workgroup
     p.x_lds = n * rows_x_stride(range) <= kRowsXBytes;
   }
-  if (!p.x_lds) split(32 * kMidWaves, (h_in + 127) / 128, 2, kMidResident, 1.5);
+  // beside one chunk's shrink (a batch of several chunks has runs, as a rule): 64
+  // tokens, 64 adapters of ranks 8 to 64, 2048 -> 2 x 8192 34 us a call with a round
+  // of 128, 41 of 256; 50 tokens, 32 adapters of rank 64, 4096 -> 2 x 4096 bf16 42
+  // with 192, 54 with 256; 177 tokens in runs of 29, 4160 -> 5440 48 and 54
+  if (!p.x_lds) split(32 * kMidWaves, (h_in + 127) / 128, 2, kMidResident - p.units, 1.5);
   return p;
 }
 
@@ -131,8 +138,10 @@ BatchCut cut_batch(int n_proj, int32_t n, int32_t h_in, int32_t h_out) {
   return rows < tiles && n <= kRowsMaxTokens ? BatchCut{0, n} : BatchCut{n, 0};
 }
 
-size_t rows_ws_bytes(WKind kind, int n_proj, int32_t n, int32_t h_in, int32_t h_out) {
-  return rows_bytes(rows_plan(kind, n_proj, n, h_in, h_out, SIZE_MAX).splits, n_proj, n, h_out);
+size_t rows_ws_bytes(WKind kind, int n_proj, int32_t n, int32_t slots, int32_t h_in, int32_t h_out) {
+  const int with = rows_plan(kind, n_proj, n, slots, h_in, h_out, SIZE_MAX).splits;
+  const int without = rows_plan(kind, n_proj, n, 0, h_in, h_out, SIZE_MAX).splits;
+  return rows_bytes(std::max(with, without), n_proj, n, h_out);
 }
 
 lora_status launch_shrink(const BaseCall& c, int splits, hipStream_t s) {
@@ -146,13 +155,12 @@ lora_status launch_shrink(const BaseCall& c, int splits, hipStream_t s) {
 lora_status launch_rows(const BaseCall& c, hipStream_t s) {
   RowsArgs a = rows_args(c);
   const int n_proj = c.glu ? 2 : 1;
-  const RowsPlan p = rows_plan(c.kind, n_proj, c.n, c.h_in, c.h_out, c.ws_bytes);
+  const RowsPlan p = rows_plan(c.kind, n_proj, c.n, c.ids ? c.pv.n_slots : 0, c.h_in, c.h_out, c.ws_bytes);
   a.splits = p.splits;
   if (c.ids || p.splits > 1) a.part = c.ws;
   if (c.ids) {
     a.t = c.ws + static_cast<int64_t>(p.splits) * n_proj * c.n * c.h_out;
-    const int units = std::min(c.n, 16 * p.tb) * n_proj * ((c.pv.max_rank + 15) / 16);
-    a.n_units = (units + 7) / 8 * 8;
+    a.n_units = p.units;
   }
   if (c.glu) {
     switch (c.kind) {

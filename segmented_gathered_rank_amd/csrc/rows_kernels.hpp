@@ -21,8 +21,8 @@
 // s (sum q x - z sum x), with the sum of x over the group formed beside it.
 //
 // Adapters.  t = s_a x A_a^T is the same kind of product with A's rank rows
-// as the weights; its workgroups come first in the grid, one for each 16-row
-// block of each distinct adapter of a chunk's tokens.  Base sums and t then go
+// as the weights; its workgroups come first in the grid, one for each distinct
+// adapter of a chunk's tokens and projection.  Base sums and t then go
 // through the workspace to a second, small kernel (k_rows_finish) that adds t B,
 // applies the gate and rounds once.  A call without adapters writes y from the
 // first kernel unless h_in is split.
@@ -114,21 +114,25 @@ __device__ __forceinline__ bool rows_distinct(int mine, bool valid, int d, int* 
 
 template <int T, int NW>   // 16-token blocks a pass over K takes at most, waves
 struct RowsShrinkShared {
-  int32_t pid[16][kRowsMaxPpr];
+  int32_t pid[kMaxRank][kRowsMaxPpr];
   int32_t tok[kRowsTokens];
   f32x4 red[NW][T][64];
 };
 
-// t of one 16-row block of adapter e for the n_tok tokens listed in sh.tok.
+// t of the rbs 16-row blocks of adapter e from block rb0 on, for the n_tok tokens
+// listed in sh.tok.  Each block goes to an equal share of the waves, which split
+// h_in.
 template <int T, int TM, int NW>
-__device__ __forceinline__ void rows_shrink_block(const RowsArgs& a, RowsShrinkShared<TM, NW>& sh, const SlotEntry& e,
-                                                  int p, int rb, int tok0, int n_tok, int lane, int wave) {
+__device__ __forceinline__ void rows_shrink_entry(const RowsArgs& a, RowsShrinkShared<TM, NW>& sh, const SlotEntry& e,
+                                                  int p, int rb0, int rbs, int tok0, int n_tok, int lane, int wave) {
   constexpr int U = T == 1 ? 8 : 4;
   const int l16 = lane & 15, lq = lane >> 4;
   const int h = static_cast<int>(a.pv.page_elems);
   const __bf16* pages = static_cast<const __bf16*>(a.pv.pages);
+  const int share = NW / rbs, rb = wave / share, part = wave - rb * share;
   const int n32 = a.h_in >> 5;
-  const int s0 = n32 * wave / NW, s1 = n32 * (wave + 1) / NW;
+  const int s0 = n32 * part / share, s1 = rb < rbs ? n32 * (part + 1) / share : s0;   // waves left over: nothing
+  const int row = min(16 * rb + l16, kMaxRank - 1);
   int tok[T];
   const __bf16* xr[T];
   f32x4 acc[T];
@@ -147,7 +151,7 @@ __device__ __forceinline__ void rows_shrink_block(const RowsArgs& a, RowsShrinkS
       // past the wave's end the last step is read again and A counts as zero: a
       // branch around the products would pull the loads into it, one by one
       const int su = min(s + u, s1 - 1);
-      af[u] = *reinterpret_cast<const u32x4*>(pages + static_cast<int64_t>(sh.pid[l16][kp]) * h + off + 8 * lq);
+      af[u] = *reinterpret_cast<const u32x4*>(pages + static_cast<int64_t>(sh.pid[row][kp]) * h + off + 8 * lq);
 #pragma unroll
       for (int tb = 0; tb < T; ++tb) xf[u][tb] = *reinterpret_cast<const bf16x8*>(xr[tb] + 32 * su);
       if (su + 1 < s1) {
@@ -166,46 +170,51 @@ __device__ __forceinline__ void rows_shrink_block(const RowsArgs& a, RowsShrinkS
 #pragma unroll
   for (int tb = 0; tb < T; ++tb) sh.red[wave][tb][lane] = acc[tb];
   __syncthreads();
-#pragma unroll
-  for (int tb = 0; tb < T; ++tb) {
-    if (wave != tb || 16 * tb + l16 >= n_tok) continue;
-    f32x4 v = sh.red[0][tb][lane];
-#pragma unroll
-    for (int w = 1; w < NW; ++w) v += sh.red[w][tb][lane];
-    float* to = a.t + (static_cast<int64_t>(p) * a.n + tok0 + tok[tb]) * kRowsTRow + 16 * rb + 4 * lq;
+  for (int it = wave; it < rbs * T; it += NW) {
+    const int b = it / T, tb = it - b * T, i = 16 * tb + l16;
+    if (i >= n_tok) continue;
+    f32x4 v = sh.red[b * share][tb][lane];
+    for (int w = 1; w < share; ++w) v += sh.red[b * share + w][tb][lane];
+    float* to = a.t + (static_cast<int64_t>(p) * a.n + tok0 + sh.tok[i]) * kRowsTRow + 16 * (rb0 + b) + 4 * lq;
     *reinterpret_cast<f32x4*>(to) = v * e.scale;
   }
 }
 
-// Shrink unit `unit` of the chunk of tokens tok0 .. tok0 + m - 1: (distinct
-// adapter, projection, 16-row block).  Whole workgroup; false when the chunk
-// has no such adapter (nor any later one).
+// Shrink unit `unit` of the chunk of tokens tok0 .. tok0 + m - 1: a distinct
+// adapter and projection, or one 16-row block of it where the chunk has so few
+// adapters that the grid's units go round (177 tokens in runs of 29, 4160 ->
+// 5440, ranks up to 64: 54 us a call against 63 with whole adapters; 64 tokens, 64
+// adapters of ranks 8 to 64, 2048 -> 2 x 8192: 41 us with whole adapters against
+// 46 with a workgroup for each block).  Whole workgroup.
 template <int TM, int NW>
-__device__ __forceinline__ bool rows_shrink(const RowsArgs& a, RowsShrinkShared<TM, NW>& sh, int unit, int n_proj,
+__device__ __forceinline__ void rows_shrink(const RowsArgs& a, RowsShrinkShared<TM, NW>& sh, int unit, int n_proj,
                                             int tok0, int m) {
   // uniform: the matrix instructions ignore the execution mask, so what they
   // depend on must be a branch of the whole wave
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int rbs = (a.pv.max_rank + 15) >> 4;
-  const int d = unit / (n_proj * rbs), rest = unit - d * (n_proj * rbs);
-  const int p = rest / rbs, rb = rest - p * rbs;
   const int mine = lane < m ? a.ids[tok0 + lane] : -1;
+  const bool valid = mine >= 0 && mine < a.pv.n_slots;
   int id;
   uint64_t same;
-  if (!rows_distinct(mine, mine >= 0 && mine < a.pv.n_slots, d, &id, &same)) return false;
+  int per = (a.pv.max_rank + 15) >> 4;   // units of an adapter and projection
+  if (per > 1 && rows_distinct(mine, valid, a.n_units / (n_proj * per), &id, &same)) per = 1;
+  const int d = unit / (n_proj * per), rest = unit - d * (n_proj * per);
+  const int p = rest / per, rb0 = rest - p * per;
+  if (!rows_distinct(mine, valid, d, &id, &same)) return;
   const SlotEntry e = a.pv.entries[static_cast<int64_t>(id) * a.pv.n_modules + a.module[p]];
-  if (e.rank <= 16 * rb) return true;
+  const int rank = __builtin_amdgcn_readfirstlane(e.rank);   // uniform, as `wave` is
+  const int rbs = per > 1 ? 1 : (rank + 15) >> 4;            // row blocks of this unit
+  if (rank <= 16 * rb0) return;
   const int n_tok = __popcll(same);
   if (wave == 0 && (same >> lane & 1)) sh.tok[__popcll(same & ((uint64_t(1) << lane) - 1))] = lane;
   const int ppr = a.h_in / static_cast<int>(a.pv.page_elems);
-  for (int q = threadIdx.x; q < 16 * ppr; q += 64 * NW) {
-    const int r = q / ppr, kp = q - r * ppr, j = 16 * rb + r;
+  for (int q = threadIdx.x; q < 16 * rbs * ppr; q += 64 * NW) {
+    const int r = q / ppr, kp = q - r * ppr, j = 16 * rb0 + r;
     sh.pid[r][kp] = j < e.rank ? a.pv.page_ids[e.a_off + j * ppr + kp] : a.pv.zero_page;
   }
   __syncthreads();
-  if (TM == 1 || n_tok <= 16) rows_shrink_block<1, TM, NW>(a, sh, e, p, rb, tok0, n_tok, lane, wave);
-  else rows_shrink_block<TM, TM, NW>(a, sh, e, p, rb, tok0, n_tok, lane, wave);
-  return true;
+  if (TM == 1 || n_tok <= 16) rows_shrink_entry<1, TM, NW>(a, sh, e, p, rb0, rbs, tok0, n_tok, lane, wave);
+  else rows_shrink_entry<TM, TM, NW>(a, sh, e, p, rb0, rbs, tok0, n_tok, lane, wave);
 }
 
 // t of every token of a long batch, for the tiled kernels.  A workgroup takes 64
@@ -418,7 +427,7 @@ __global__ __launch_bounds__(kRowsThreads) void k_rows(RowsArgs a) {
   __shared__ Shared sh;
   const int m = a.n;   // at most 16
   if (static_cast<int>(blockIdx.x) < a.n_units) {
-    if (blockIdx.z == 0) (void)rows_shrink<1, kRowsWaves>(a, sh.shrink, blockIdx.x, NP, 0, m);
+    if (blockIdx.z == 0) rows_shrink<1, kRowsWaves>(a, sh.shrink, blockIdx.x, NP, 0, m);
     return;
   }
   // consecutive column blocks on one XCD, so that they share lines of the scales in its L2
@@ -604,8 +613,7 @@ __global__ __launch_bounds__(kRowsThreads) void k_rows(RowsArgs a) {
 // 2 x 12288: 30 to 31 us; one block to a wave 34 to 42, 4 or 16 waves and other
 // depths no better).  With GLU a wave takes a gate block and the up block of the
 // same columns.  Measured: that case with zero points and adapters 34 us
-// (1.5 TB/s of codes and scales); fp8, 64 tokens, 2048 -> 2 x 8192 with 64
-// adapters of ranks 8 to 64 32 us, 16 to 18 of them the weights'.
+// (1.5 TB/s of codes and scales).
 //
 // x in LDS: rows of 256 bytes whose 16-byte chunks are XORed with the row, so
 // that the 16 rows of a fragment read cover all banks once.
@@ -642,7 +650,7 @@ __global__ __launch_bounds__(kMidThreads, 3) void k_mid(RowsArgs a) {
   if (b < 0) {
     const int chunk = blockIdx.x / a.n_units, at = chunk * 16 * TB;
     if (blockIdx.z == 0)
-      (void)rows_shrink<TB, kMidThreads / 64>(a, sh.shrink, blockIdx.x - chunk * a.n_units, NP, at, min(a.n - at, 16 * TB));
+      rows_shrink<TB, kMidThreads / 64>(a, sh.shrink, blockIdx.x - chunk * a.n_units, NP, at, min(a.n - at, 16 * TB));
     return;
   }
   const int xcd = b & 7;
