@@ -21,13 +21,18 @@ struct RowsPlan {
 // Workgroups that the GPU holds at a time: k_rows two to a CU, k_mid one.
 constexpr int kRowsResident = 512;
 constexpr int kMidResident = 256;
+constexpr int kShrinkUnits = 128;   // shrink workgroups of a launch, about
 
 // adapters: how many different ones the batch may hold (0: a call without ids).
 RowsPlan rows_plan(WKind kind, int n_proj, int32_t n, int32_t adapters, int32_t h_in, int32_t h_out, size_t ws_bytes) {
   RowsPlan p{};
   p.tb = n > 48 ? 4 : (n + 15) / 16;
   p.chunks = (n + 16 * p.tb - 1) / (16 * p.tb);
-  p.units = (std::min({n, 16 * p.tb, adapters}) * n_proj + 7) / 8 * 8;
+  // Each takes an adapter and projection at a time.  The chunks of a longer batch
+  // have runs, as a rule, and workgroups without work are not free: 512 tokens in
+  // runs of 128, 4096 -> 4096 59 us a call with 16 to a chunk, 74 with 64; 1000
+  // tokens, 768 -> 2 x 2304 69 and 83.
+  p.units = (std::min(std::min({n, 16 * p.tb, adapters}) * n_proj, std::max(kShrinkUnits / p.chunks, 16)) + 7) / 8 * 8;
   // the split of h_in with the least rounds of workgroups times steps of each,
   // at `step` microseconds a step, 4 to start a workgroup, and the sums' way
   // through the workspace (a call, split against unsplit: 64 tokens, 4096 ->
@@ -55,11 +60,12 @@ RowsPlan rows_plan(WKind kind, int n_proj, int32_t n, int32_t adapters, int32_t 
     const int range = ((steps + p.splits - 1) / p.splits + 1) * ks;   // at most, of one workgroup
     p.x_lds = n * rows_x_stride(range) <= kRowsXBytes;
   }
-  // beside one chunk's shrink (a batch of several chunks has runs, as a rule): 64
-  // tokens, 64 adapters of ranks 8 to 64, 2048 -> 2 x 8192 34 us a call with a round
-  // of 128, 41 of 256; 50 tokens, 32 adapters of rank 64, 4096 -> 2 x 4096 bf16 42
-  // with 192, 54 with 256; 177 tokens in runs of 29, 4160 -> 5440 48 and 54
-  if (!p.x_lds) split(32 * kMidWaves, (h_in + 127) / 128, 2, kMidResident - p.units, 1.5);
+  // beside the shrink: 64 tokens, 64 adapters of ranks 8 to 64, 2048 -> 2 x 8192 fp8
+  // 34 us a call with rounds of 128, 41 of 256; 50 tokens, 32 adapters of rank 64,
+  // 4096 -> 2 x 4096 bf16 42 with 192, 54 with 256; 177 tokens in runs of 29, 4160 ->
+  // 5440 50 with 192, 55 with 208
+  const int beside = adapters == 0 ? 0 : p.chunks > 1 ? kShrinkUnits / 2 : p.units;
+  if (!p.x_lds) split(32 * kMidWaves, (h_in + 127) / 128, 2, kMidResident - beside, 1.5);
   return p;
 }
 
@@ -108,10 +114,10 @@ RowsArgs rows_args(const BaseCall& c) {
 // The kernels' measured costs in microseconds.  Rows: 10 to start, 0.45 for each
 // 10^6 weights and chunk of 64 tokens, 6 for each 10^6 base sums written and
 // read.  Tiles: 35 to start (with the shrink) and 0.032 for each k of every round
-// of 256 tiles.  Measured, rows against tiles: 4096x4096 4-bit 67 / 154 at 512
-// tokens, 118 / 157 at 1024; 4096 -> 2 x 12288 bf16 113 / 154 at 128, 206 / 128
-// at 256; 768 -> 2 x 2304 4-bit 45 / 60 at 512, 83 / 62 at 1024; 2048 -> 2 x 8192
-// fp8, ranks up to 64, 83 / 143 at 256, 154 / 144 at 512.  A few tokens past a
+// of 256 tiles.  Measured, rows against tiles: 4096x4096 4-bit 59 / 154 at 512
+// tokens, 99 / 156 at 1000; 4096 -> 2 x 12288 bf16 115 / 153 at 128, 207 / 128 at
+// 256; 768 -> 2 x 2304 4-bit 42 / 60 at 512, 69 / 64 at 1000; 2048 -> 2 x 8192 fp8,
+// ranks up to 64, 82 / 143 at 256, 141 / 146 at 512.  A few tokens past a
 // multiple of 256 may add a round of tiles for a batch's rest that rows take in
 // less: 4096 -> 2 x 8192 fp8, 2111 tokens as 2048 + 63 take 350 us, where 2304,
 // as many tiles as 2111 alone would be, take 410.

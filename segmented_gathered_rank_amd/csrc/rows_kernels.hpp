@@ -183,11 +183,12 @@ __device__ __forceinline__ void rows_shrink_entry(const RowsArgs& a, RowsShrinkS
 // Shrink unit `unit` of the chunk of tokens tok0 .. tok0 + m - 1: a distinct
 // adapter and projection, or one 16-row block of it where the chunk has so few
 // adapters that the grid's units go round (177 tokens in runs of 29, 4160 ->
-// 5440, ranks up to 64: 54 us a call against 63 with whole adapters; 64 tokens, 64
+// 5440, ranks up to 64: 54 us a call, 63 with whole adapters; 64 tokens, 64
 // adapters of ranks 8 to 64, 2048 -> 2 x 8192: 41 us with whole adapters against
-// 46 with a workgroup for each block).  Whole workgroup.
+// 46 with a workgroup for each block).  Whole workgroup; false when the chunk has
+// no such adapter (nor any later one).
 template <int TM, int NW>
-__device__ __forceinline__ void rows_shrink(const RowsArgs& a, RowsShrinkShared<TM, NW>& sh, int unit, int n_proj,
+__device__ __forceinline__ bool rows_shrink(const RowsArgs& a, RowsShrinkShared<TM, NW>& sh, int unit, int n_proj,
                                             int tok0, int m) {
   // uniform: the matrix instructions ignore the execution mask, so what they
   // depend on must be a branch of the whole wave
@@ -200,11 +201,11 @@ __device__ __forceinline__ void rows_shrink(const RowsArgs& a, RowsShrinkShared<
   if (per > 1 && rows_distinct(mine, valid, a.n_units / (n_proj * per), &id, &same)) per = 1;
   const int d = unit / (n_proj * per), rest = unit - d * (n_proj * per);
   const int p = rest / per, rb0 = rest - p * per;
-  if (!rows_distinct(mine, valid, d, &id, &same)) return;
+  if (!rows_distinct(mine, valid, d, &id, &same)) return false;
   const SlotEntry e = a.pv.entries[static_cast<int64_t>(id) * a.pv.n_modules + a.module[p]];
   const int rank = __builtin_amdgcn_readfirstlane(e.rank);   // uniform, as `wave` is
   const int rbs = per > 1 ? 1 : (rank + 15) >> 4;            // row blocks of this unit
-  if (rank <= 16 * rb0) return;
+  if (rank <= 16 * rb0) return true;
   const int n_tok = __popcll(same);
   if (wave == 0 && (same >> lane & 1)) sh.tok[__popcll(same & ((uint64_t(1) << lane) - 1))] = lane;
   const int ppr = a.h_in / static_cast<int>(a.pv.page_elems);
@@ -215,6 +216,14 @@ __device__ __forceinline__ void rows_shrink(const RowsArgs& a, RowsShrinkShared<
   __syncthreads();
   if (TM == 1 || n_tok <= 16) rows_shrink_entry<1, TM, NW>(a, sh, e, p, rb0, rbs, tok0, n_tok, lane, wave);
   else rows_shrink_entry<TM, TM, NW>(a, sh, e, p, rb0, rbs, tok0, n_tok, lane, wave);
+  return true;
+}
+
+// The units of a chunk that workgroup `first` of its a.n_units takes.
+template <int TM, int NW>
+__device__ __forceinline__ void rows_shrink_all(const RowsArgs& a, RowsShrinkShared<TM, NW>& sh, int first, int n_proj,
+                                                int tok0, int m) {
+  for (int unit = first; rows_shrink<TM, NW>(a, sh, unit, n_proj, tok0, m); unit += a.n_units) __syncthreads();
 }
 
 // t of every token of a long batch, for the tiled kernels.  A workgroup takes 64
@@ -427,7 +436,7 @@ __global__ __launch_bounds__(kRowsThreads) void k_rows(RowsArgs a) {
   __shared__ Shared sh;
   const int m = a.n;   // at most 16
   if (static_cast<int>(blockIdx.x) < a.n_units) {
-    if (blockIdx.z == 0) rows_shrink<1, kRowsWaves>(a, sh.shrink, blockIdx.x, NP, 0, m);
+    if (blockIdx.z == 0) rows_shrink_all<1, kRowsWaves>(a, sh.shrink, blockIdx.x, NP, 0, m);
     return;
   }
   // consecutive column blocks on one XCD, so that they share lines of the scales in its L2
@@ -650,7 +659,8 @@ __global__ __launch_bounds__(kMidThreads, 3) void k_mid(RowsArgs a) {
   if (b < 0) {
     const int chunk = blockIdx.x / a.n_units, at = chunk * 16 * TB;
     if (blockIdx.z == 0)
-      rows_shrink<TB, kMidThreads / 64>(a, sh.shrink, blockIdx.x - chunk * a.n_units, NP, at, min(a.n - at, 16 * TB));
+      rows_shrink_all<TB, kMidThreads / 64>(a, sh.shrink, blockIdx.x - chunk * a.n_units, NP, at,
+                                            min(a.n - at, 16 * TB));
     return;
   }
   const int xcd = b & 7;
