@@ -69,8 +69,8 @@ lora_status base_call(const lora_pool* p, BaseCall& c, const int32_t* module, co
   if (ws_bytes > 0 && (!ws || !aligned(ws, 16))) return LORA_ERR_ARG;
   if (n_tokens == 0) return LORA_OK;
   const int64_t h_in = p->h_in[module[0]];
-  const BatchCut cut = cut_batch(n_proj, n_tokens, static_cast<int32_t>(h_in),
-                                 static_cast<int32_t>(h_out));
+  const BatchCut cut =
+      cut_batch(n_proj, n_tokens, static_cast<int32_t>(h_in), static_cast<int32_t>(h_out), p->max_rank);
   if (cut.tiles > 0 && !tiles_fit(c.glu, cut.tiles, static_cast<int32_t>(h_out))) return LORA_ERR_SHAPE;
   if (ids && ws_bytes < ws_need(cut, n_proj, h_in, h_out)) return LORA_ERR_WORKSPACE;
   DeviceGuard g(p->device);
@@ -114,7 +114,7 @@ extern "C" {
 size_t lora_fused_workspace_bytes(const lora_pool* p, int32_t module, int32_t n_proj, int32_t n_tokens) {
   if (!p || module < 0 || module >= p->n_modules || n_proj < 1 || n_proj > 2 || n_tokens < 1) return 0;
   const int32_t h_in = static_cast<int32_t>(p->h_in[module]), h_out = static_cast<int32_t>(p->h_out[module]);
-  const BatchCut cut = cut_batch(n_proj, n_tokens, h_in, h_out);
+  const BatchCut cut = cut_batch(n_proj, n_tokens, h_in, h_out, p->max_rank);
   size_t most = cut.tiles > 0 ? tiles_ws_bytes(n_proj, cut.tiles, h_in) : 0;
   if (cut.rows > 0)   // over the kinds of weights, as the call is not known
     for (WKind kind : {WKind::kBf16, WKind::kFp8, WKind::kInt4})

@@ -36,7 +36,7 @@ size_t rows_ws_bytes(WKind kind, int n_proj, int32_t n_tokens, int32_t slots, in
 struct BatchCut {
   int32_t tiles, rows;
 };
-BatchCut cut_batch(int n_proj, int32_t n_tokens, int32_t h_in, int32_t h_out);   // rows.hip
+BatchCut cut_batch(int n_proj, int32_t n_tokens, int32_t h_in, int32_t h_out, int32_t max_rank);   // rows.hip
 
 // Workspace of the tiled kernels: t of every token from each split of h_in.
 // The splits fill the GPU once, with 64 tokens and at least 256 k to each
