@@ -43,8 +43,8 @@ BatchCut cut_batch(int n_proj, int32_t n_tokens, int32_t h_in, int32_t h_out, in
 // workgroup; the tiles add them up.
 constexpr int kTilesMaxSplits = 4;
 inline int tiles_splits(int32_t n_tokens, int32_t h_in) {
-  const int chunks = (n_tokens + 63) / 64;
-  int s = 256 / chunks;
+  const int64_t chunks = (static_cast<int64_t>(n_tokens) + 63) / 64;
+  int s = static_cast<int>(256 / chunks);
   if (s > kTilesMaxSplits) s = kTilesMaxSplits;
   if (s > h_in / 256) s = h_in / 256;
   return s < 1 ? 1 : s;

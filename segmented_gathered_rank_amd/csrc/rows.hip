@@ -126,7 +126,7 @@ RowsArgs rows_args(const BaseCall& c) {
 // 2048 + 63 take 350 us, where 2304, as many tiles as 2111 alone would be, take 410.
 double rows_cost(int n_proj, int32_t n, int32_t h_in, int32_t h_out) {
   const double cols = static_cast<double>(n_proj) * h_out;
-  return 10.0 + 0.4e-6 * cols * h_in * ((n + 63) / 64) + 6e-6 * n * cols;
+  return 10.0 + 0.4e-6 * cols * h_in * ((static_cast<int64_t>(n) + 63) / 64) + 6e-6 * n * cols;
 }
 double tiles_cost(int n_proj, int32_t n, int32_t h_in, int32_t h_out, int32_t max_rank) {
   const int64_t cols = static_cast<int64_t>(n_proj) * h_out;

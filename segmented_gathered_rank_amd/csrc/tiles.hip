@@ -26,8 +26,10 @@ int64_t n_tiles(bool glu, int32_t n, int32_t h_out) {
 
 }  // namespace
 
-// 512 threads to a tile: within a launch's 2^32 - 1.
-bool tiles_fit(bool glu, int32_t n, int32_t h_out) { return n_tiles(glu, n, h_out) <= (int64_t(1) << 22); }
+// 512 threads to a tile, and to 64 tokens of the shrink: within a launch's 2^32 - 1.
+bool tiles_fit(bool glu, int32_t n, int32_t h_out) {
+  return n <= (1 << 28) && n_tiles(glu, n, h_out) <= (int64_t(1) << 22);
+}
 
 lora_status launch_tiles(const BaseCall& c, hipStream_t s) {
   FusedArgs a{};

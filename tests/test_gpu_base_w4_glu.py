@@ -378,3 +378,18 @@ def test_refusals_of_pools_and_pairs():
     assert status(lambda: sgr.lora_fused_gemm_w4(f32, 0, t, 128, w, None, 1, t, 128)) == -6
     sgr.lora_pool_destroy(pool)
     sgr.lora_pool_destroy(f32)
+
+
+@pytest.mark.parametrize("n", [(1 << 28) + 256, (1 << 31) - 1])
+def test_batches_past_a_launch(n):
+    """Refused before anything is launched; the workspace query counts them all the same."""
+    p = Problem("gemm", "int4", 4, 256, 64, group=64, ranks=(16,), seed=51)
+    g = Problem("glu", "bf16", 4, 256, 64, ranks=(16,), seed=52)
+    assert sgr.lora_fused_workspace_bytes(p.pool, 0, 1, n) == 4 * n * 64
+    for q in (p, g):
+        with pytest.raises(sgr.LoraError) as ei:
+            q.call(n=n)
+        assert ei.value.status == -2
+        torch.cuda.synchronize()
+        assert bool((q.y == SENTINEL).all())
+        q.close()
