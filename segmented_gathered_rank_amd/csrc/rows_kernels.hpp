@@ -622,14 +622,15 @@ __global__ __launch_bounds__(kRowsThreads) void k_rows(RowsArgs a) {
 // and k for every workgroup) stay below W's, and read their own rows of W
 // straight into registers, D - 1 steps ahead.  Loads return in order, so waves
 // that waited for x would wait for all of W's steps too: that is why other waves
-// bring it.  What bounds the kernel is the issue of instructions and the
-// registers, so those waves also put x in the order the widening likes, form the
-// sums of it that the zero points multiply and bring the scales, and a fragment
-// of x that was read from LDS meets two blocks (33 tokens, 4-bit, 4096 ->
-// 2 x 12288: 30 to 31 us; one block to a wave 34 to 42, 4 or 16 waves and other
-// depths no better).  With GLU a wave takes a gate block and the up block of the
-// same columns.  Measured: that case with zero points and adapters 34 us
-// (1.5 TB/s of codes and scales).
+// bring it.  What bounds the kernel is a mix: the vector ALU issues in 39% of the
+// SIMDs' cycles (MFMA busy 17%), and three waves to a SIMD, all that the registers
+// allow, leave the rest to barriers and loads.  So the bringing waves also put x in
+// the order the widening likes, form the sums of it that the zero points multiply
+// and bring the scales, and a fragment of x that was read from LDS meets two
+// blocks (33 tokens, 4-bit, 4096 -> 2 x 12288, without adapters: 30 to 31 us when
+// tried; one block to a wave 34 to 42, 4 or 16 waves and other depths no better).  With GLU a wave takes a gate block and the up block of the
+// same columns.  Measured: that case with zero points and adapters 29 us
+// (1.9 TB/s of codes and scales).
 //
 // x in LDS: rows of 256 bytes whose 16-byte chunks are XORed with the row, so
 // that the 16 rows of a fragment read cover all banks once.
@@ -705,6 +706,11 @@ __global__ __launch_bounds__(kMidThreads, 3) void k_mid(RowsArgs a) {
   struct Step {
     u32x4 w[L][CB];
   };
+  // A step of 4-bit codes is half a line of each row, so the line has to stay for
+  // the next step: plain loads (33 tokens, 4096 -> 2 x 12288 29 us, 33 with
+  // streaming ones).  A step of 8 or 16 bits is whole lines: streaming, so that
+  // the adapters' pages stay (64 tokens, 2048 -> 2 x 8192 fp8: the finish 12 us
+  // against 14).
   auto load_w = [&](Step& t, int s) {
 #pragma unroll
     for (int l = 0; l < L; ++l) {
@@ -713,7 +719,7 @@ __global__ __launch_bounds__(kMidThreads, 3) void k_mid(RowsArgs a) {
       const int at = s * (64 * L) + 64 * l, over = max(at + 16 * lq + 16 - row_bytes, 0);
       const uint32_t off = w_lane + static_cast<uint32_t>(at - over);   // the row's start or later: no wrap
 #pragma unroll
-      for (int cb = 0; cb < CB; ++cb) t.w[l][cb] = ld16<true>(reinterpret_cast<const u32x4*>(wp[cb] + off));
+      for (int cb = 0; cb < CB; ++cb) t.w[l][cb] = ld16<!W4>(reinterpret_cast<const u32x4*>(wp[cb] + off));
     }
   };
   if (wave >= kMidWaves) {
