@@ -9,7 +9,6 @@ zero point per group, "table" with a 16-entry codebook), the widths, the batch
 and its adapters.
 """
 import math
-import weakref
 
 import torch
 
@@ -121,7 +120,7 @@ class _Pool:
 
     def __init__(self, case, a, b, scales):
         import segmented_gathered_rank_amd as sgr
-        m, page = _projections(case), case["page"]
+        self.sgr, m, page = sgr, _projections(case), case["page"]
         ranks = _ranks(case)
         pages = sum(ranks) * (case["h_in"] + case["h_out"]) // page * m
         self.h = sgr.lora_pool_create(torch.cuda.current_device(), sgr.LORA_BF16, page, pages, case["slots"], m,
@@ -131,7 +130,9 @@ class _Pool:
                 sgr.lora_pool_load(self.h, s, p, r, a[p][s, :r].contiguous(), b[p][s, :r].contiguous(),
                                    float(scales[s]))
         torch.cuda.synchronize()
-        weakref.finalize(self, sgr.lora_pool_destroy, self.h)   # also at exit, while the library is there
+
+    def __del__(self):
+        self.sgr.lora_pool_destroy(self.h)
 
 
 def prepare(case, seed):
