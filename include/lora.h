@@ -434,6 +434,14 @@ lora_status lora_fused_gemm_fp8w(const lora_pool *p, int32_t module,
  * captured graphs that may run at the same time need one each. */
 size_t lora_fused_workspace_bytes(const lora_pool *p, int32_t module, int32_t n_proj, int32_t n_tokens);
 
+/* Which way a call of the four entry points below takes: its first tokens, as
+ * many as this returns, run on tiles of 256, the rest stream the weights' rows
+ * (either may be none).  The ways differ in the order of their fp32 sums and in
+ * what is said at lora_fused_gemm_w4, so a token's last bit may.  w_bits is 4, 8
+ * or 16, with_ids whether the call has ids; -1 on bad arguments. */
+int32_t lora_fused_tile_tokens(const lora_pool *p, int32_t module, int32_t n_proj, int32_t w_bits,
+                               int32_t n_tokens, int32_t with_ids);
+
 /* Base weights of one projection as 4-bit codes with a scale per output column
  * and group of `group` consecutive k (study page, section "Operating it": a
  * quantized base serves under the bf16 adapters; its table of adapter kinds

@@ -23,6 +23,7 @@ __all__ = [
     "LORA_NOALLOC_SCRATCH_BYTES",
     "lora_expand", "lora_apply_sgmv", "lora_apply_sgmv_multi", "lora_x_run", "lora_apply_bgmv", "lora_apply_bgmv_ids", "lora_apply_bgmv_packed", "lora_fused_gemm", "lora_fused_gemm_fp8w",
     "LORA_ACT_SILU", "LORA_ACT_GELU", "LORA_ACT_GELU_TANH", "lora_w4", "lora_w4_bind", "lora_fused_workspace_bytes",
+    "lora_fused_tile_tokens",
     "lora_fused_gemm_w4", "lora_fused_glu", "lora_fused_glu_fp8w", "lora_fused_glu_w4",
     "LORA_TIER_GPU", "LORA_TIER_HOST", "LORA_TIER_COLD", "lora_tiers_create", "lora_tiers_destroy",
     "lora_tiers_touch", "lora_tiers_stats", "lora_tiers_slot_of", "lora_tiers_acquire",
@@ -119,6 +120,7 @@ _SIGS = {
     "lora_fused_gemm": (_I32, [_P, _I32, _P, _I64, _P, _I64, _P, _I32, _P, _I64, _P]),
     "lora_fused_gemm_fp8w": (_I32, [_P, _I32, _P, _I64, _P, _I64, _P, _P, _I32, _P, _I64, _P]),
     "lora_fused_workspace_bytes": (_SZ, [_P, _I32, _I32, _I32]),
+    "lora_fused_tile_tokens": (_I32, [_P, _I32, _I32, _I32, _I32, _I32]),
     "lora_fused_gemm_w4": (_I32, [_P, _I32, _P, _I64, _W4P, _P, _I32, _P, _I64, _P, _SZ, _P]),
     "lora_fused_glu": (_I32, [_P, _I32, _I32, _P, _I64, _P, _P, _I64, _P, _I32, _I32, _P, _I64, _P, _SZ, _P]),
     "lora_fused_glu_fp8w": (_I32, [_P, _I32, _I32, _P, _I64, _P, _P, _I64, _P, _P, _P, _I32, _I32, _P, _I64, _P,
@@ -357,6 +359,11 @@ def _ws_bytes(ws, ws_bytes: int) -> int:
 
 def lora_fused_workspace_bytes(pool: int, module: int, n_proj: int, n_tokens: int) -> int:
     return int(_lib.lora_fused_workspace_bytes(pool, module, n_proj, n_tokens))
+
+
+def lora_fused_tile_tokens(pool: int, module: int, n_proj: int, w_bits: int, n_tokens: int, with_ids: bool) -> int:
+    """How many of a call's first tokens run on tiles; -1 on bad arguments."""
+    return int(_lib.lora_fused_tile_tokens(pool, module, n_proj, w_bits, n_tokens, int(with_ids)))
 
 
 def lora_fused_gemm_w4(pool: int, module: int, x, ld_x: int, w: lora_w4, ids, n_tokens: int, y, ld_y: int, ws=None,

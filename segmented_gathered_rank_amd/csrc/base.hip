@@ -19,6 +19,11 @@ size_t ws_need(const BatchCut& cut, int n_proj, int64_t h_in, int64_t h_out) {
                   cut.tiles > 0 ? tiles_ws_bytes(n_proj, cut.tiles, static_cast<int32_t>(h_in)) : 0);
 }
 
+BaseShape shape_of(const lora_pool* p, int32_t module, WKind kind, int n_proj, bool with_ids) {
+  return BaseShape{kind, n_proj, static_cast<int32_t>(p->h_in[module]), static_cast<int32_t>(p->h_out[module]),
+                   with_ids ? p->n_slots : 0, p->max_rank};
+}
+
 bool aligned(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
 // Checks of everything but the weights, for one projection or a pair.
@@ -69,8 +74,7 @@ lora_status base_call(const lora_pool* p, BaseCall& c, const int32_t* module, co
   if (ws_bytes > 0 && (!ws || !aligned(ws, 16))) return LORA_ERR_ARG;
   if (n_tokens == 0) return LORA_OK;
   const int64_t h_in = p->h_in[module[0]];
-  const BatchCut cut =
-      cut_batch(n_proj, n_tokens, static_cast<int32_t>(h_in), static_cast<int32_t>(h_out), p->max_rank);
+  const BatchCut cut = cut_batch(shape_of(p, module[0], c.kind, n_proj, ids != nullptr), n_tokens);
   if (cut.tiles > 0 && !tiles_fit(c.glu, cut.tiles, static_cast<int32_t>(h_out))) return LORA_ERR_SHAPE;
   if (ids && ws_bytes < ws_need(cut, n_proj, h_in, h_out)) return LORA_ERR_WORKSPACE;
   DeviceGuard g(p->device);
@@ -114,12 +118,23 @@ extern "C" {
 size_t lora_fused_workspace_bytes(const lora_pool* p, int32_t module, int32_t n_proj, int32_t n_tokens) {
   if (!p || module < 0 || module >= p->n_modules || n_proj < 1 || n_proj > 2 || n_tokens < 1) return 0;
   const int32_t h_in = static_cast<int32_t>(p->h_in[module]), h_out = static_cast<int32_t>(p->h_out[module]);
-  const BatchCut cut = cut_batch(n_proj, n_tokens, h_in, h_out, p->max_rank);
-  size_t most = cut.tiles > 0 ? tiles_ws_bytes(n_proj, cut.tiles, h_in) : 0;
-  if (cut.rows > 0)   // over the kinds of weights, as the call is not known
-    for (WKind kind : {WKind::kBf16, WKind::kFp8, WKind::kInt4})
-      most = std::max(most, rows_ws_bytes(kind, n_proj, cut.rows, p->n_slots, h_in, h_out));
+  size_t most = 0;   // over the kinds of weights and with or without ids, as the call is not known
+  for (WKind kind : {WKind::kBf16, WKind::kFp8, WKind::kInt4})
+    for (bool with_ids : {false, true}) {
+      const BatchCut cut = cut_batch(shape_of(p, module, kind, n_proj, with_ids), n_tokens);
+      if (cut.tiles > 0 && with_ids) most = std::max(most, tiles_ws_bytes(n_proj, cut.tiles, h_in));
+      if (cut.rows > 0) most = std::max(most, rows_ws_bytes(kind, n_proj, cut.rows, with_ids ? p->n_slots : 0, h_in, h_out));
+    }
   return most;
+}
+
+int32_t lora_fused_tile_tokens(const lora_pool* p, int32_t module, int32_t n_proj, int32_t w_bits, int32_t n_tokens,
+                               int32_t with_ids) {
+  if (!p || module < 0 || module >= p->n_modules || n_proj < 1 || n_proj > 2 || n_tokens < 0 ||
+      (w_bits != 4 && w_bits != 8 && w_bits != 16))
+    return -1;
+  const WKind kind = w_bits == 4 ? WKind::kInt4 : w_bits == 8 ? WKind::kFp8 : WKind::kBf16;
+  return cut_batch(shape_of(p, module, kind, n_proj, with_ids != 0), n_tokens).tiles;
 }
 
 lora_status lora_fused_gemm_w4(const lora_pool* p, int32_t module, const void* x, int64_t ld_x, const lora_w4* w,

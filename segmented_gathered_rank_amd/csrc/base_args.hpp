@@ -2,21 +2,13 @@
 // 4-bit codes' widening, and the gate's activations.
 #pragma once
 
+#include "base_plan.hpp"
 #include "common.hpp"
 
 namespace lora {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-
-// Storage of W^T ([h_out] rows along h_in).
-enum class WKind : int {
-  kBf16,    // bf16
-  kFp8,     // OCP e4m3 codes, one float scale per row
-  kInt4,    // 4-bit codes q: s (q - z), s and z per row and group of `group` k (no z array: 8)
-  kTable4   // 4-bit codes q: s T[q], T a 16-entry bf16 codebook
-};
-constexpr bool is_w4(WKind k) { return k == WKind::kInt4 || k == WKind::kTable4; }
 
 // The base weights of one projection.
 struct WView {

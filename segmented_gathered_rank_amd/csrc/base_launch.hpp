@@ -29,14 +29,8 @@ constexpr int kRowsMaxSplits = 8;
 inline size_t rows_bytes(int splits, int n_proj, int32_t n_tokens, int64_t h_out) {
   return sizeof(float) * n_proj * static_cast<size_t>(n_tokens) * static_cast<size_t>(splits * h_out + kMaxRank);
 }
-// What a call uses when it is given as much as it can use.
-size_t rows_ws_bytes(WKind kind, int n_proj, int32_t n_tokens, int32_t slots, int32_t h_in, int32_t h_out);
-// A batch's first `tiles` tokens take tiles (fused_gemm.hpp), the `rows` after
-// them stream W's rows (rows_kernels.hpp); either may be 0.
-struct BatchCut {
-  int32_t tiles, rows;
-};
-BatchCut cut_batch(int n_proj, int32_t n_tokens, int32_t h_in, int32_t h_out, int32_t max_rank);   // rows.hip
+// What a call uses when it is given as much as it can use (adapters: 0 without ids).
+size_t rows_ws_bytes(WKind kind, int n_proj, int32_t n_tokens, int32_t adapters, int32_t h_in, int32_t h_out);
 
 // Workspace of the tiled kernels: t of every token from each split of h_in.
 // The splits fill the GPU once, with 64 tokens and at least 256 k to each

@@ -111,46 +111,8 @@ RowsArgs rows_args(const BaseCall& c) {
 
 }  // namespace
 
-// The kernels' measured costs in microseconds.  Rows: 10 to start, 0.4 for each
-// 10^6 weights and chunk of 64 tokens, 6 for each 10^6 base sums written and
-// read.  Tiles: 35 to start (with the shrink), 0.032 for each k of every round of
-// 256 tiles, and 12 for each projection and 16 ranks past the first 16 that an
-// adapter may have (a tile meets two or three adapters where the batch has runs;
-// a batch of unlike neighbours costs tiles far more, 1150 us for 1000 tokens of 64
-// adapters at the last shape below, which the host does not see).  Measured, rows
-// against tiles: 4096x4096 4-bit 59 / 154 at 512 tokens, 99 / 156 at 1000; 4096 ->
-// 2 x 12288 bf16 115 / 153 at 128, 207 / 128 at 256; 768 -> 2 x 2304 4-bit 42 / 60
-// at 512, 69 / 64 at 1000; 2048 -> 2 x 8192 fp8, ranks up to 64, 82 / 143 at 256,
-// 131 / 143 at 512.  A few tokens past a multiple of 256 may add a round of tiles
-// for a batch's rest that rows take in less: 4096 -> 2 x 8192 fp8, 2111 tokens as
-// 2048 + 63 take 350 us, where 2304, as many tiles as 2111 alone would be, take 410.
-double rows_cost(int n_proj, int32_t n, int32_t h_in, int32_t h_out) {
-  const double cols = static_cast<double>(n_proj) * h_out;
-  return 10.0 + 0.4e-6 * cols * h_in * ((static_cast<int64_t>(n) + 63) / 64) + 6e-6 * n * cols;
-}
-double tiles_cost(int n_proj, int32_t n, int32_t h_in, int32_t h_out, int32_t max_rank) {
-  const int64_t cols = static_cast<int64_t>(n_proj) * h_out;
-  const int64_t n_tiles = (static_cast<int64_t>(n) + 255) / 256 * ((cols + 255) / 256);
-  return 35.0 + 12.0 * n_proj * ((max_rank - 1) / 16) + 0.032 * h_in * static_cast<double>((n_tiles + 255) / 256);
-}
-
-// Longest batch of the row-streaming kernels: the finish has a grid row for each token.
-constexpr int32_t kRowsMaxTokens = 32768;
-
-BatchCut cut_batch(int n_proj, int32_t n, int32_t h_in, int32_t h_out, int32_t max_rank) {
-  if (n <= kRowsTokens) return {0, n};
-  const double rows = rows_cost(n_proj, n, h_in, h_out), tiles = tiles_cost(n_proj, n, h_in, h_out, max_rank);
-  const int32_t tail = n % 256, whole = n - tail;
-  if (tail > 0 && whole > 0 &&
-      tiles_cost(n_proj, whole, h_in, h_out, max_rank) + rows_cost(n_proj, tail, h_in, h_out) < std::min(rows, tiles))
-    return {whole, tail};
-  return rows < tiles && n <= kRowsMaxTokens ? BatchCut{0, n} : BatchCut{n, 0};
-}
-
-size_t rows_ws_bytes(WKind kind, int n_proj, int32_t n, int32_t slots, int32_t h_in, int32_t h_out) {
-  const int with = rows_plan(kind, n_proj, n, slots, h_in, h_out, SIZE_MAX).splits;
-  const int without = rows_plan(kind, n_proj, n, 0, h_in, h_out, SIZE_MAX).splits;
-  return rows_bytes(std::max(with, without), n_proj, n, h_out);
+size_t rows_ws_bytes(WKind kind, int n_proj, int32_t n, int32_t adapters, int32_t h_in, int32_t h_out) {
+  return rows_bytes(rows_plan(kind, n_proj, n, adapters, h_in, h_out, SIZE_MAX).splits, n_proj, n, h_out);
 }
 
 lora_status launch_shrink(const BaseCall& c, int splits, hipStream_t s) {
