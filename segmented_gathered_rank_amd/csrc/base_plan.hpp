@@ -40,10 +40,15 @@ struct BaseShape {
 // 6 for each 10^6 base sums written and read.  Tiles: 35 to start (with the
 // shrink), 0.032 for each k of every round of 256 tiles, and 12 for each projection
 // and 16 ranks past the first 16 that an adapter may have (a tile meets two or
-// three adapters where the batch has runs).  Measured, rows against tiles:
+// three adapters where the batch has runs).  The host does not see the ids, and a
+// batch whose neighbours differ costs tiles about 4 for each round, projection and
+// 16 ranks of every adapter that a tile may meet: 0.2 is charged of it, as if one
+// batch in twenty were such, so that where the ways are close rows, which take
+// any order alike, are taken.  Measured, rows against tiles:
 // 4096x4096 4-bit 58 / 156 at 512 tokens, 97 / 157 at 1000; 4096 -> 2 x 12288 bf16
 // 204 / 127 at 256; 768 -> 2 x 2304 4-bit 42 / 60 at 512, 69 / 64 at 1000; 2048 ->
-// 2 x 8192 fp8, ranks up to 64, 84 / 143 at 256, 140 / 145 at 512.
+// 2 x 8192 fp8, ranks up to 64, 84 / 143 at 256, 140 / 145 at 512.  With unlike
+// neighbours of 64 adapters: the third shape 98 / 553 at 1000, the second 209 / 697.
 //
 // Without ids there is no shrink, no expand and, on rows, no finish unless h_in is
 // split.  Rows: 10, 0.33, 0.2 or 0.19 for each 10^6 weights of 16, 8 or 4 bits and
@@ -70,7 +75,8 @@ inline double tiles_cost(const BaseShape& b, int32_t n) {
   const int64_t n_tiles = (static_cast<int64_t>(n) + 255) / 256 * ((cols + 255) / 256);
   const double rounds = static_cast<double>((n_tiles + 255) / 256);
   if (b.adapters == 0) return 15.0 + 0.03 * b.h_in * rounds;
-  return 35.0 + 12.0 * b.n_proj * ((b.max_rank - 1) / 16) + 0.032 * b.h_in * rounds;
+  const int units = b.n_proj * std::min(b.adapters, 256) * ((b.max_rank + 15) / 16);   // that a tile may meet
+  return 35.0 + 12.0 * b.n_proj * ((b.max_rank - 1) / 16) + (0.032 * b.h_in + 0.2 * units) * rounds;
 }
 
 inline BatchCut cut_batch(const BaseShape& b, int32_t n) {

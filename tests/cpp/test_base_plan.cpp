@@ -1,6 +1,7 @@
 // Host unit test of the cut of a batch between the row-streaming and the tiled
 // base products (built with g++ under AddressSanitizer and
 // UndefinedBehaviorSanitizer by tests/test_base_plan.py).
+#include <algorithm>
 #include <cstdint>
 #include <cstdio>
 
@@ -72,6 +73,71 @@ int main() {
       const BatchCut c = cut(s.kind, s.n_proj, s.h_in, s.h_out, 0, rank, s.n);
       CHECK(s.rows_us < s.tiles_us ? c.rows == s.n : c.tiles >= s.n / 256 * 256);
     }
+
+  // ---- with ids: measured us a call, a batch in runs on rows / on tiles and one of unlike neighbours on rows / on
+  // tiles.  The host does not know which batch it has: the way taken costs at most a quarter more than the better one
+  // when one batch in sixteen is of unlike neighbours.
+  struct WithIds {
+    WKind kind;
+    int n_proj;
+    int32_t h_in, h_out, adapters, max_rank, n;
+    int runs_rows, runs_tiles, unlike_rows, unlike_tiles;
+  };
+  const WithIds w[] = {
+      {WKind::kTable4, 2, 768, 2304, 64, 16, 512, 42, 60, 64, 555},
+      {WKind::kTable4, 2, 768, 2304, 64, 64, 512, 51, 103, 72, 1057},
+      {WKind::kTable4, 2, 768, 2304, 8, 16, 512, 41, 60, 40, 117},
+      {WKind::kTable4, 2, 768, 2304, 64, 16, 1000, 69, 64, 98, 553},
+      {WKind::kTable4, 2, 768, 2304, 64, 64, 1000, 78, 110, 109, 1037},
+      {WKind::kTable4, 2, 768, 2304, 8, 16, 1000, 67, 63, 63, 121},
+      {WKind::kTable4, 2, 768, 2304, 64, 16, 2048, 117, 67, 180, 546},
+      {WKind::kTable4, 2, 768, 2304, 64, 64, 2048, 133, 112, 201, 1028},
+      {WKind::kTable4, 2, 768, 2304, 8, 16, 2048, 114, 67, 109, 124},
+      {WKind::kInt4, 1, 4096, 4096, 64, 16, 512, 58, 156, 66, 447},
+      {WKind::kInt4, 1, 4096, 4096, 64, 64, 512, 64, 177, 86, 721},
+      {WKind::kInt4, 1, 4096, 4096, 8, 16, 512, 50, 154, 50, 188},
+      {WKind::kInt4, 1, 4096, 4096, 64, 16, 1000, 97, 157, 108, 442},
+      {WKind::kInt4, 1, 4096, 4096, 64, 64, 1000, 97, 170, 133, 731},
+      {WKind::kInt4, 1, 4096, 4096, 8, 16, 1000, 93, 157, 81, 188},
+      {WKind::kInt4, 1, 4096, 4096, 64, 16, 2048, 177, 159, 193, 448},
+      {WKind::kInt4, 1, 4096, 4096, 64, 64, 2048, 173, 172, 241, 748},
+      {WKind::kInt4, 1, 4096, 4096, 8, 16, 2048, 148, 158, 143, 188},
+      {WKind::kFp8, 2, 2048, 8192, 64, 16, 512, 116, 96, 124, 628},
+      {WKind::kFp8, 2, 2048, 8192, 64, 64, 512, 140, 145, 158, 1165},
+      {WKind::kFp8, 2, 2048, 8192, 8, 16, 512, 115, 97, 101, 159},
+      {WKind::kFp8, 2, 2048, 8192, 64, 16, 1000, 204, 100, 229, 625},
+      {WKind::kFp8, 2, 2048, 8192, 64, 64, 1000, 238, 148, 277, 1153},
+      {WKind::kFp8, 2, 2048, 8192, 8, 16, 1000, 201, 100, 179, 161},
+      {WKind::kFp8, 2, 2048, 8192, 64, 16, 2048, 403, 185, 471, 1094},
+      {WKind::kFp8, 2, 2048, 8192, 64, 64, 2048, 428, 238, 534, 2046},
+      {WKind::kFp8, 2, 2048, 8192, 8, 16, 2048, 395, 183, 385, 283},
+      {WKind::kBf16, 2, 4096, 12288, 64, 16, 256, 204, 127, 209, 697},
+      {WKind::kBf16, 2, 4096, 12288, 64, 64, 256, 229, 174, 225, 1276},
+      {WKind::kBf16, 2, 4096, 12288, 8, 16, 256, 207, 127, 205, 195},
+      {WKind::kBf16, 2, 4096, 12288, 64, 16, 512, 338, 133, 385, 686},
+      {WKind::kBf16, 2, 4096, 12288, 64, 64, 512, 367, 176, 426, 1243},
+      {WKind::kBf16, 2, 4096, 12288, 8, 16, 512, 335, 135, 321, 198},
+      {WKind::kBf16, 2, 4096, 12288, 64, 16, 1000, 630, 258, 694, 1148},
+      {WKind::kBf16, 2, 4096, 12288, 64, 64, 1000, 647, 312, 807, 2091},
+      {WKind::kBf16, 2, 4096, 12288, 8, 16, 1000, 628, 255, 613, 359},
+      {WKind::kBf16, 2, 4096, 12288, 64, 16, 2048, 1306, 426, 1468, 1620},
+      {WKind::kBf16, 2, 4096, 12288, 64, 64, 2048, 1341, 484, 1593, 2899},
+      {WKind::kBf16, 2, 4096, 12288, 8, 16, 2048, 1310, 421, 1284, 549},
+      {WKind::kInt4, 1, 2048, 5120, 64, 16, 512, 60, 90, 68, 361},
+      {WKind::kInt4, 1, 2048, 5120, 64, 64, 512, 67, 111, 74, 617},
+      {WKind::kInt4, 1, 2048, 5120, 8, 16, 512, 44, 90, 43, 122},
+      {WKind::kInt4, 1, 2048, 5120, 64, 16, 1000, 97, 96, 103, 358},
+      {WKind::kInt4, 1, 2048, 5120, 64, 64, 1000, 104, 116, 124, 613},
+      {WKind::kInt4, 1, 2048, 5120, 8, 16, 1000, 79, 94, 76, 125},
+      {WKind::kInt4, 1, 2048, 5120, 64, 16, 2048, 160, 99, 175, 359},
+      {WKind::kInt4, 1, 2048, 5120, 64, 64, 2048, 159, 111, 217, 621},
+      {WKind::kInt4, 1, 2048, 5120, 8, 16, 2048, 141, 97, 131, 126},
+  };
+  for (const WithIds& s : w) {
+    const BatchCut c = cut(s.kind, s.n_proj, s.h_in, s.h_out, s.adapters, s.max_rank, s.n);
+    const double rows = 15 * s.runs_rows + s.unlike_rows, tiles = 15 * s.runs_tiles + s.unlike_tiles;
+    CHECK((c.rows == s.n ? rows : tiles) <= 1.25 * std::min(rows, tiles));
+  }
   std::puts("base plan ok");
   return 0;
 }
