@@ -394,6 +394,8 @@ lora_status lora_apply_bgmv_packed(const lora_pool *p, int32_t module0, int32_t 
  * tile costs about 16/256 of its base part per 16 rank rows of each
  * distinct adapter among its 256 tokens, so batches whose tiles mix many
  * adapters (decode) belong on lora_apply_bgmv after a plain GEMM.
+ * An infinity or NaN in an adapter's A or B makes outputs of that adapter's own
+ * tokens non-finite (B: those of its column, as NaN) and no others.
  * The pool must be bf16 and h_in / page_elems at most 32.
  * Errors: ARG (null pointer, bad module, n_tokens < 0, a leading dimension
  * below the width, misalignment), DTYPE (pool not bf16), SHAPE, HIP. */
@@ -471,7 +473,8 @@ typedef struct {
  * and the exact v; sums, scales and the adapter term are fp32 (on the tiled
  * path t is multiplied by B as two bf16 parts of 16 significand bits), and y
  * is rounded once.  A non-finite value in a row of x makes that row's outputs
- * non-finite and no other's.  y must not overlap x, the weights or ws.
+ * non-finite and no other's, and one in an adapter's A or B reaches that adapter's
+ * tokens only.  y must not overlap x, the weights or ws.
  * Short batches (decode) stream the weights' rows once per 64 tokens, in one
  * launch, or two with ids or with h_in split, through `ws`
  * (lora_fused_workspace_bytes); long ones run on tiles of 256 tokens, behind a
