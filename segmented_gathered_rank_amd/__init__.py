@@ -338,14 +338,41 @@ def lora_fused_gemm_fp8w(pool: int, module: int, x, ld_x: int, w8, ld_w: int, w_
                                      n_tokens, _ptr(y), ld_y, _stream(stream)), "lora_fused_gemm_fp8w")
 
 
+def _w4_tensor(name: str, t, dtype: str, ndim: int) -> None:
+    if str(getattr(t, "dtype", None)) != "torch." + dtype or t.dim() != ndim:
+        raise ValueError(f"{name} has to be a {dtype} tensor of {ndim} dimension{'s' * (ndim > 1)}")
+    if t.numel() > 0 and t.stride(-1) != 1:
+        raise ValueError(f"the rows of {name} must be dense")
+
+
 def lora_w4_bind(codes, scale, group: int, zero=None, table=None) -> lora_w4:
-    """4-bit weights of one projection from its device tensors (codes [h_out][ld] uint8, scale
-    and zero [h_in / group][ld]; rows dense); the returned struct keeps them alive."""
+    """4-bit weights of one projection from its device tensors: codes [h_out][>= h_in / 2] uint8, scale
+    [h_in / group][>= h_out] bfloat16, zero uint8 as scale, table [16] bfloat16; rows dense.  ValueError
+    where they are something else or do not belong together; the returned struct keeps them alive."""
+    if group not in (32, 64, 128):
+        raise ValueError("group has to be 32, 64 or 128")
+    if zero is not None and table is not None:
+        raise ValueError("either zero or table")
+    _w4_tensor("codes", codes, "uint8", 2)
+    _w4_tensor("scale", scale, "bfloat16", 2)
+    n_g, h_out = scale.shape[0], codes.shape[0]
+    if n_g < 1 or scale.shape[1] < h_out:
+        raise ValueError(f"scale has to hold {h_out} columns, as many as codes has rows, for each group")
+    if 2 * codes.shape[1] < n_g * group:
+        raise ValueError(f"codes has to hold the {n_g * group} codes of scale's groups in each row")
+    if zero is not None:
+        _w4_tensor("zero", zero, "uint8", 2)
+        if zero.shape[0] < n_g or zero.shape[1] < h_out:
+            raise ValueError("zero has to hold as many groups and columns as scale")
+        if n_g > 1 and zero.stride(0) != scale.stride(0):
+            raise ValueError("zero and scale need one row stride")
+    if table is not None:
+        _w4_tensor("table", table, "bfloat16", 1)
+        if table.numel() != 16:
+            raise ValueError("table has to hold 16 values")
     for t in (codes, scale, zero, table):
-        if t is not None and t.stride(-1) != 1:
-            raise ValueError("the rows of codes, scale, zero and table must be dense")
-    if zero is not None and zero.stride(0) != scale.stride(0):
-        raise ValueError("zero and scale need one row stride")
+        if t is not None and (not t.is_cuda or t.device != codes.device):
+            raise ValueError("codes, scale, zero and table have to be on one GPU")
     w = lora_w4(_ptr(codes), codes.stride(0), _ptr(scale), _ptr(zero), scale.stride(0), _ptr(table), group)
     w._keep = (codes, scale, zero, table)
     return w
