@@ -105,9 +105,11 @@ typedef struct {
  *   h_in,h_out  [host] [n_modules] input/output widths; multiples of page_elems
  *   max_rank    rank cap, 1..LORA_MAX_RANK
  * An entry spans at most max_rank * (h_in + h_out) / page_elems pages, which
- * may be up to 8192.  Pools with a module above 1024 (small pages under wide
- * modules and high ranks) serve the fused passes only: lora_shrink,
- * lora_expand and the lora_apply calls return LORA_ERR_SHAPE for them.
+ * may be up to 1024, or up to 8192 in a bf16 pool whose module has at most 32
+ * pages to a row of A (h_in / page_elems).  Pools with a module above 1024 (small
+ * pages under wide modules and high ranks) serve the fused passes only:
+ * lora_shrink, lora_expand and the lora_apply calls return LORA_ERR_SHAPE for
+ * them, their other modules too.
  * On success *out holds the pool.  Synchronous.  Errors: ARG, SHAPE, RANK, HIP. */
 lora_status lora_pool_create(lora_pool **out, int32_t device, lora_dtype wdtype,
                              int64_t page_elems, int64_t n_pages, int32_t n_slots,

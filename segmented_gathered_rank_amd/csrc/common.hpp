@@ -20,6 +20,7 @@ constexpr int kMaxRank = LORA_MAX_RANK;
 constexpr int kMaxSlots = 8192;   // the segment builder's LDS histogram bound
 constexpr int kMaxEntryPages = 1024;  // pages of one (slot, module) entry the apply kernels serve (an LDS table in the GEMV ones)
 constexpr int kMaxPoolEntryPages = 8192;  // pages of one entry a pool accepts (the fused passes read any)
+constexpr int kMaxFusedRowPages = 32;  // pages of one rank row of A (h_in / page_elems) the fused passes serve
 
 // One (slot, module) entry of the device slot table.
 struct SlotEntry {

@@ -68,7 +68,7 @@ constexpr int kFgBN = 256;        // output columns per tile
 constexpr int kFgBK = 64;         // k per pipeline step
 constexpr int kFgTileBytes = kFgBM * kFgBK * 2;   // one [256][64] bf16 tile
 constexpr int kFgPassUnits = 2;   // 16-rank units per pass over K, at most
-constexpr int kFgMaxPpr = 32;     // A pages per rank row (h_in / page_elems) at most
+constexpr int kFgMaxPpr = kMaxFusedRowPages;   // A pages per rank row (h_in / page_elems) at most
 constexpr int kFgMaxBpages = 8;   // B pages a tile's 256 columns touch, at most (page >= 64)
 constexpr int kFgMaxSlots = 8192; // slot ids a tile's bitmap covers
 constexpr int kFgMaxUnits = kFgBM * 4;   // 256 distinct adapters x 4 units (rank 64), per projection

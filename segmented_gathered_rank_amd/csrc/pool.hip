@@ -259,7 +259,9 @@ lora_status lora_pool_create(lora_pool** out, int32_t device, lora_dtype wdtype,
     if (h_in[m] * page_elems >= (int64_t(1) << 32) || h_out[m] * page_elems >= (int64_t(1) << 32))
       return LORA_ERR_SHAPE;
     const int64_t ppe = static_cast<int64_t>(max_rank) * (h_in[m] + h_out[m]) / page_elems;
-    if (ppe > kMaxPoolEntryPages) return LORA_ERR_SHAPE;
+    // wider entries are for the fused passes, which take bf16 and so many pages to a row of A
+    const bool fused = wdtype == LORA_BF16 && h_in[m] / page_elems <= kMaxFusedRowPages;
+    if (ppe > (fused ? kMaxPoolEntryPages : kMaxEntryPages)) return LORA_ERR_SHAPE;
     if (ppe > max_ppe) max_ppe = ppe;
     if (h_in[m] > max_in) max_in = h_in[m];
     if (h_out[m] > max_out) max_out = h_out[m];

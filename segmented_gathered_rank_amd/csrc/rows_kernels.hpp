@@ -38,7 +38,7 @@ constexpr int kMidWaves = 8;       // waves of k_mid that multiply
 constexpr int kMidMovers = 4;      // and that bring x
 constexpr int kMidCols = 32 * kMidWaves;   // rows of W^T of a workgroup
 constexpr int kMidThreads = 64 * (kMidWaves + kMidMovers);
-constexpr int kRowsMaxPpr = 32;    // A pages per rank row
+constexpr int kRowsMaxPpr = kMaxFusedRowPages;   // A pages per rank row
 constexpr int kRowsTRow = kMaxRank;
 
 constexpr int kRowsXBytes = 64 * 1024;   // x in LDS: two workgroups to a CU
