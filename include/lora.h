@@ -471,12 +471,16 @@ typedef struct {
  *   t_i[j] = sum_k x_i[k] A_a[j][k],  a = ids[i],
  * W as lora_w4 says.  x, ids, the adapters and y are as for lora_fused_gemm
  * (y is written for every token; ids NULL: x W alone; a token whose id is -1,
- * out of range or of an empty slot gets x_i W alone).  Products are of bf16 x
- * and the exact v; sums, scales and the adapter term are fp32 (on the tiled
- * path t is multiplied by B as two bf16 parts of 16 significand bits), and y
- * is rounded once.  A non-finite value in a row of x makes that row's outputs
- * non-finite and no other's, and one in an adapter's A or B reaches that adapter's
- * tokens only.  y must not overlap x, the weights or ws.
+ * out of range or of an empty slot gets x_i W alone).  Sums, scales and the
+ * adapter term are fp32, and y is rounded once.  On tiles products are of bf16 x
+ * and the exact v, and t is multiplied by B as two bf16 parts of 16 significand
+ * bits.  Where the weights' rows are streamed a table's products are the same,
+ * t is fp32, and integers take their zero point z (8 without `zero`) after the
+ * products of each group, as s (sum q x - z sum x): the roundings of those fp32
+ * sums are relative to s sum (q + z) |x| and not to s sum |q - z| |x|, and an x
+ * beyond 1e34 may overflow there.  A non-finite value in a row of x makes that
+ * row's outputs non-finite and no other's, and one in an adapter's A or B reaches
+ * that adapter's tokens only.  y must not overlap x, the weights or ws.
  * Short batches (decode) stream the weights' rows once per 64 tokens, in one
  * launch, or two with ids or with h_in split, through `ws`
  * (lora_fused_workspace_bytes); long ones run on tiles of 256 tokens, behind a
