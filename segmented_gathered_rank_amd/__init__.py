@@ -5,7 +5,7 @@ function here has the C function's name and arguments, takes tensors (or raw
 integer device pointers) and the current HIP stream, and raises LoraError
 when the C call returns a non-zero status.  All computation happens in the
 HIP library; there is no fallback of any kind.  Importing this package fails
-if the library has not been built (``python -m segmented_gathered_rank_amd.build``).
+if the library has not been built (``python segmented_gathered_rank_amd/build.py``).
 """
 from __future__ import annotations
 
@@ -58,7 +58,7 @@ except ImportError:
     pass
 
 if not os.path.exists(LIB_PATH):
-    raise ImportError(f"{LIB_PATH} is missing: build it with `python -m segmented_gathered_rank_amd.build`")
+    raise ImportError(f"{LIB_PATH} is missing: build it with `python segmented_gathered_rank_amd/build.py`")
 _lib = ctypes.CDLL(LIB_PATH)
 
 

@@ -1,6 +1,6 @@
 """Builds the HIP library liblora_mi355x.so in-tree (gfx950 only).
 
-    python -m segmented_gathered_rank_amd.build
+    python segmented_gathered_rank_amd/build.py
 
 Each .hip source is compiled to an object with hipcc, then linked into one
 shared library next to this file.  Packed-fp32 instruction forms are turned
