@@ -59,8 +59,8 @@ struct BaseShape {
 // 35 / 44 at 1000, 54 / 47 at 2048.
 //
 // A few tokens past a multiple of 256 may add a round of tiles for a batch's rest
-// that rows take in less: 4096 -> 2 x 8192 fp8, 2111 tokens as 2048 + 63 take 325
-// us, where 2304, as many tiles as 2111 alone would be, took 410.
+// that rows take in less: 4096 -> 2 x 8192 fp8, 2111 tokens as 2048 + 63 take 343
+// us, where 2304, as many tiles as 2111 alone would be, take 416.
 inline double rows_cost(const BaseShape& b, int32_t n) {
   const double cols = static_cast<double>(b.n_proj) * b.h_out;
   const double chunks = static_cast<double>((static_cast<int64_t>(n) + kRowsTokens - 1) / kRowsTokens);

@@ -30,14 +30,14 @@ RowsPlan rows_plan(WKind kind, int n_proj, int32_t n, int32_t adapters, int32_t 
   p.chunks = (n + 16 * p.tb - 1) / (16 * p.tb);
   // Each takes an adapter and projection at a time.  The chunks of a longer batch
   // have runs, as a rule, and workgroups without work are not free: 512 tokens in
-  // runs of 128, 4096 -> 4096 59 us a call with 16 to a chunk, 74 with 64; 1000
-  // tokens, 768 -> 2 x 2304 69 and 83.
+  // runs of 128, 4096 -> 4096 56 us a call with 16 to a chunk, 68 with 64; 1000
+  // tokens, 768 -> 2 x 2304 66 and 74.
   p.units = (std::min(std::min({n, 16 * p.tb, adapters}) * n_proj, std::max(kShrinkUnits / p.chunks, 16)) + 7) / 8 * 8;
   // the split of h_in with the least rounds of workgroups times steps of each,
   // at `step` microseconds a step, 4 to start a workgroup, and the sums' way
   // through the workspace (a call, split against unsplit: 64 tokens, 4096 ->
-  // 4096 4-bit 18 us in 8 splits against 61; 33 tokens, 4096 -> 2 x 12288 4-bit 40
-  // in 2 against 60)
+  // 4096 4-bit 19 us in 8 splits against 61; 33 tokens, 4096 -> 2 x 12288 4-bit 34
+  // in 2 against 51)
   auto split = [&](int cols, int steps, int min_steps, int resident, double step) {
     p.blocks = (h_out * n_proj + cols - 1) / cols;
     const double sums = 2e-6 * n * n_proj * h_out;
@@ -63,7 +63,7 @@ RowsPlan rows_plan(WKind kind, int n_proj, int32_t n, int32_t adapters, int32_t 
   // beside the shrink: 64 tokens, 64 adapters of ranks 8 to 64, 2048 -> 2 x 8192 fp8
   // 34 us a call with rounds of 128, 41 of 256; 50 tokens, 32 adapters of rank 64,
   // 4096 -> 2 x 4096 bf16 42 with 192, 54 with 256; 177 tokens in runs of 29, 4160 ->
-  // 5440 50 with 192, 55 with 208
+  // 5440 48 with 192, 52 with 208
   const int beside = adapters == 0 ? 0 : p.chunks > 1 ? kShrinkUnits / 2 : p.units;
   if (!p.x_lds) split(32 * kMidWaves, (h_in + 127) / 128, 2, kMidResident - beside, 1.5);
   return p;

@@ -182,9 +182,9 @@ __device__ __forceinline__ void rows_shrink_entry(const RowsArgs& a, RowsShrinkS
 // Shrink unit `unit` of the chunk of tokens tok0 .. tok0 + m - 1: a distinct
 // adapter and projection, or one 16-row block of it where the chunk has so few
 // adapters that the grid's units go round (177 tokens in runs of 29, 4160 ->
-// 5440, ranks up to 64: 54 us a call, 63 with whole adapters; 64 tokens, 64
-// adapters of ranks 8 to 64, 2048 -> 2 x 8192: 41 us with whole adapters against
-// 46 with a workgroup for each block).  Whole workgroup; false when the chunk has
+// 5440, ranks up to 64: 49 us a call, 65 with whole adapters; 64 tokens, 64
+// adapters of ranks 8 to 64, 2048 -> 2 x 8192: 34 us with whole adapters against
+// 40 with a workgroup for each block).  Whole workgroup; false when the chunk has
 // no such adapter (nor any later one).
 template <int TM, int NW>
 __device__ __forceinline__ bool rows_shrink(const RowsArgs& a, RowsShrinkShared<TM, NW>& sh, int unit, int n_proj,
@@ -422,10 +422,10 @@ __device__ __forceinline__ bf16x8 rows_fp8(u32x4 v, int h) {
 // h_in is split between gridDim.z workgroups and their waves, each of which
 // reads U loads of each of its rows one batch ahead of the products.  x waits
 // in LDS: loads return in order, so x loaded in between would hold up W.
-// Bound by the read of W: bf16, 1 token, 4096 -> 2 x 11264 37 us (5.0 TB/s);
-// 4-bit with zero points, 1 token, 8192 -> 28672 35 us (3.4 TB/s, where the
+// Bound by the read of W: bf16, 1 token, 4096 -> 2 x 11264 36 us (5.1 TB/s);
+// 4-bit with zero points, 1 token, 8192 -> 28672 35 us (3.5 TB/s, where the
 // widening's and scaling's instructions are as long as the read); small layers
-// by the launch (4-bit, 768 -> 768 5.3 us).
+// by the launch (4-bit, 768 -> 768 5.4 us).
 template <WKind WK, int G, int CB, bool GLU>
 __global__ __launch_bounds__(kRowsThreads) void k_rows(RowsArgs a) {
   constexpr int F = RowsLoad<WK>::kFrags, KS = RowsLoad<WK>::kK;
@@ -629,7 +629,7 @@ __global__ __launch_bounds__(kRowsThreads) void k_rows(RowsArgs a) {
 // blocks (33 tokens, 4-bit, 4096 -> 2 x 12288, without adapters: 30 to 31 us when
 // tried; one block to a wave 34 to 42, 4 or 16 waves and other depths no better).  With GLU a wave takes a gate block and the up block of the
 // same columns.  Measured: that case with zero points and adapters 29 us
-// (1.9 TB/s of codes and scales).
+// (1.8 TB/s of codes and scales).
 //
 // x in LDS: rows of 256 bytes whose 16-byte chunks are XORed with the row, so
 // that the 16 rows of a fragment read cover all banks once.
